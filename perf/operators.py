@@ -113,7 +113,7 @@ def _quantize(x):
     e = torch.where(amax == 0, -127, e)
     a = b.abs() * ((127 - e) << 23).to(torch.int32).view(torch.float32).unsqueeze(2)
     code = (a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0)
-    code = (code + 8 * torch.signbit(b)).view(rows, K // 2, 2)
+    code = (code + 8 * torch.signbit(b).to(torch.uint8)).view(rows, K // 2, 2)
     return code[:, :, 0] + 16 * code[:, :, 1], (e + 127).to(torch.uint8)
 
 
