@@ -1,0 +1,358 @@
+// C entry points of the MXFP4 and expert operators: argument validation, the
+// packed handle and launch planning.
+#include <algorithm>
+#include <climits>
+#include <new>
+
+#include "abi_util.h"
+#include "mx4_internal.h"
+
+using namespace spense;
+
+struct spense_mx4_packed {
+  int device = -1;
+  int64_t E = 0, N = 0, K = 0;
+  int n_tiles = 0, kblocks = 0;
+  uint8_t* blocks = nullptr;
+};
+
+namespace {
+
+constexpr size_t kMx4Workspace = 256;  // the header: status word
+
+// Rows a tile of activations takes, cluster split, ring depth.
+//
+// A tile reads its weight block and its activation rows for every 256 columns
+// of K; up to 256 rows one tile takes all of them, so that weights are read
+// once. With experts the device alone knows who has how many rows: room for
+// twice the average, since a heavier expert only costs a second reading of its
+// weights (from L2) and smaller tiles leave a deeper ring.
+//
+// Few tiles: the largest cluster of 8, 4 or 2 that two CTAs a SM can hold at
+// once, that leaves each CTA two blocks or more and room for its ring.
+spense_status make_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, Mx4GemmPlan* out) {
+  Mx4GemmPlan pl{};
+  const int64_t want = ragged ? std::max<int64_t>(2 * ((T + E - 1) / E), 32) : T;
+  pl.npad = static_cast<int>(std::min<int64_t>(256, round_up(static_cast<size_t>(std::min(want, T)), 16)));
+  const int64_t row_tiles = ragged ? std::min(E, T) + T / pl.npad : (T + pl.npad - 1) / pl.npad;
+  const int64_t tiles = row_tiles * n_tiles;
+  if (tiles > INT_MAX / 2) return fail(SPENSE_ERR_SHAPE, "too many tiles for one launch (%lld)", (long long)tiles);
+  const uint32_t atoms = (static_cast<uint32_t>(pl.npad) + 127u) / 128u;
+  pl.xs_off = kMx4BlockBytes + static_cast<uint32_t>(pl.npad) * 128u;
+  pl.stage_bytes = pl.xs_off + atoms * 1024u;
+  const uint32_t tail = static_cast<uint32_t>(round_up(256 + 4 * (3 * static_cast<size_t>(E) + 1), 16));
+  // Ring stages beside `recv` bytes of partials with `cps` CTAs a SM.
+  auto ring = [&](int cps, uint32_t recv) {
+    const uint32_t budget = cps == 2 ? 115200u : 232448u, fixed = 1024 + tail + recv;
+    return budget <= fixed ? 0 : static_cast<int>(std::min<uint32_t>(12, (budget - fixed) / pl.stage_bytes));
+  };
+  pl.split = 1;
+  pl.ctas_per_sm = 1;
+  if (pl.npad <= 64 && tiles < sms)
+    for (int s = 8; s > 1 && pl.split == 1; s >>= 1) {
+      const int cps = tiles * s > sms ? 2 : 1;
+      const int need = std::max(3, std::min(4, (kblocks + s - 1) / s));
+      if (tiles * s <= 2 * sms && kblocks >= 2 * s && ring(cps, static_cast<uint32_t>((s - 1) * pl.npad * 512)) >= need) {
+        pl.split = s;
+        pl.ctas_per_sm = cps;
+      }
+    }
+  pl.recv_bytes = static_cast<uint32_t>((pl.split - 1) * pl.npad * 512);
+  pl.grid = static_cast<int>(pl.split > 1 ? tiles * pl.split : std::min<int64_t>(tiles, sms));
+  pl.nacc = pl.split == 1 && 2 * pl.npad + 48 <= 512 ? 2 : 1;
+  pl.tmem_cols = 32;
+  while (pl.tmem_cols < static_cast<uint32_t>(pl.nacc * pl.npad + 48)) pl.tmem_cols <<= 1;
+  pl.stages = ring(pl.ctas_per_sm, pl.recv_bytes);
+  if (pl.stages < 3) return fail(SPENSE_ERR_SHAPE, "no launch plan for %lld experts", (long long)E);
+  pl.smem_bytes = 1024 + tail + pl.recv_bytes + static_cast<uint32_t>(pl.stages) * pl.stage_bytes;
+  // A CTA that takes more than half of the tensor memory has the SM to itself.
+  if (pl.tmem_cols > 256) pl.smem_bytes = std::max<uint32_t>(pl.smem_bytes, 122880u);
+  *out = pl;
+  return SPENSE_OK;
+}
+
+spense_status check_mx4_types(int64_t rows, int64_t K) {
+  if (rows < 0 || rows > kMx4MaxRows)
+    return fail(SPENSE_ERR_SHAPE, "%lld rows outside [0, 2^20]", (long long)rows);
+  if (K < 32 || K > (1 << 20) || K % 32 != 0)
+    return fail(SPENSE_ERR_SHAPE, "K = %lld must be a multiple of 32 in [32, 2^20]", (long long)K);
+  return SPENSE_OK;
+}
+
+spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8_t* x_scale, int64_t T,
+                      const int32_t* offsets, uint16_t* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  if (h == nullptr) return fail(SPENSE_ERR_ARG, "Wp is NULL");
+  if (T < 0 || T > kMx4MaxRows) return fail(SPENSE_ERR_SHAPE, "%lld rows outside [0, 2^20]", (long long)T);
+  if (T > 0 && (Xq == nullptr || x_scale == nullptr || Y == nullptr))
+    return fail(SPENSE_ERR_ARG, "Xq, x_scale or Y is NULL");
+  if (ldy < h->N || ldy > (1 << 30))
+    return fail(SPENSE_ERR_SHAPE, "ldy = %lld outside [N = %lld, 2^30]", (long long)ldy, (long long)h->N);
+  if (!aligned(Xq, 16) || !aligned(x_scale, 16) || !aligned(Y, 16))
+    return fail(SPENSE_ERR_ALIGN, "Xq, x_scale and Y must be 16-byte aligned");
+  if (workspace == nullptr) return fail(SPENSE_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(workspace, 256)) return fail(SPENSE_ERR_ALIGN, "workspace is not 256-byte aligned");
+  if (workspace_bytes < kMx4Workspace)
+    return fail(SPENSE_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", workspace_bytes, kMx4Workspace);
+  int dev = 0;
+  DeviceInfo info;
+  spense_status st = current_device(&dev, &info);
+  if (st != SPENSE_OK) return st;
+  if (dev != h->device)
+    return fail(SPENSE_ERR_ARG, "handle was packed on device %d, current device is %d", h->device, dev);
+  if (T == 0) return ok();
+  Mx4GemmPlan pl;
+  st = make_mx4_plan(h->E, h->n_tiles, h->kblocks, T, offsets != nullptr, info.sms, &pl);
+  if (st != SPENSE_OK) return st;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return fail(SPENSE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  Mx4GemmParams p{};
+  CUtensorMap maps[3];
+  for (int i = 0; i < 3; ++i) {
+    p.box[i] = std::min(pl.npad, i == 0 ? 16 : (i == 1 ? 64 : 256));
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(h->K / 2), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(h->K / 2)};
+    const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(p.box[i])};
+    const cuuint32_t estr[2] = {1u, 1u};
+    const CUresult r = encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(Xq), dims, strides, box,
+                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(SPENSE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  p.blocks = h->blocks;
+  p.xs = reinterpret_cast<const uint32_t*>(x_scale);
+  p.y = Y;
+  p.ldy = ldy;
+  p.offsets = offsets;
+  p.status = reinterpret_cast<unsigned int*>(ws);
+  p.test_gate = nullptr;
+#ifdef SPENSE_TEST_HOOKS
+  // Test build only: with SPENSE_TEST_STALL=1 the loaders wait on header word
+  // 16 of the workspace, which nothing sets, so every launch ends by timeout.
+  static const bool stall = std::getenv("SPENSE_TEST_STALL") != nullptr && std::getenv("SPENSE_TEST_STALL")[0] == '1';
+  if (stall) p.test_gate = reinterpret_cast<const unsigned int*>(ws + 64);
+#endif
+  p.E = static_cast<int>(h->E);
+  p.N = static_cast<int>(h->N);
+  p.T = static_cast<int>(T);
+  p.n_tiles = h->n_tiles;
+  p.kblocks = h->kblocks;
+  p.groups = static_cast<int>((h->K + 127) / 128);
+  const int tail_cols = static_cast<int>(h->K - static_cast<int64_t>(h->kblocks - 1) * kMx4Cols);
+  p.last_steps = (tail_cols + 63) / 64;
+  p.npad = pl.npad;
+  p.stages = pl.stages;
+  p.nacc = pl.nacc;
+  p.split = pl.split;
+  p.stage_bytes = pl.stage_bytes;
+  p.xs_off = pl.xs_off;
+  p.recv_bytes = pl.recv_bytes;
+  p.tmem_cols = pl.tmem_cols;
+  p.w_keep = T > pl.npad ? 1 : 0;
+  const cudaError_t e = launch_mx4_gemm(maps, p, pl.grid, pl.smem_bytes, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mx4 gemm launch");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+spense_status spense_mx4_quantize(const void* X, int x_type, int64_t M, int64_t K, int64_t ldx, const int32_t* rows,
+                                  int64_t T, uint8_t* Xq, uint8_t* x_scale, unsigned int flags, void* stream) {
+  if (x_type != SPENSE_TYPE_BF16 && x_type != SPENSE_TYPE_F16 && x_type != SPENSE_TYPE_F32)
+    return fail(SPENSE_ERR_ARG, "unknown x_type %d", x_type);
+  if (flags & ~static_cast<unsigned int>(SPENSE_MX4_SCALE_ROWS))
+    return fail(SPENSE_ERR_ARG, "unknown flags 0x%x", flags);
+  spense_status st = check_mx4_types(M, K);
+  if (st != SPENSE_OK) return st;
+  st = check_mx4_types(T, K);
+  if (st != SPENSE_OK) return st;
+  if (rows == nullptr && T != M)
+    return fail(SPENSE_ERR_SHAPE, "T = %lld must equal M = %lld without rows", (long long)T, (long long)M);
+  if (ldx < K || ldx > (1 << 30))
+    return fail(SPENSE_ERR_SHAPE, "ldx = %lld outside [K = %lld, 2^30]", (long long)ldx, (long long)K);
+  if (T > 0 && (Xq == nullptr || x_scale == nullptr || (M > 0 && X == nullptr)))
+    return fail(SPENSE_ERR_ARG, "X, Xq or x_scale is NULL");
+  const int64_t esize = x_type == SPENSE_TYPE_F32 ? 4 : 2;
+  if (!aligned(X, 16) || !aligned(Xq, 16) || !aligned(x_scale, 16) || !aligned(rows, 4) || (ldx * esize) % 16 != 0)
+    return fail(SPENSE_ERR_ALIGN, "X (and each of its rows), Xq and x_scale must be 16-byte aligned, rows 4-byte");
+  int dev = 0;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != SPENSE_OK) return st;
+  const cudaError_t e = launch_mx4_quantize(X, x_type, T, K, ldx, rows, M, Xq, x_scale,
+                                            (flags & SPENSE_MX4_SCALE_ROWS) == 0, info.sms,
+                                            static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mx4 quantize launch");
+  return ok();
+}
+
+spense_status spense_mx4_dequantize(const uint8_t* Xq, const uint8_t* x_scale, int64_t M, int64_t K, void* Y,
+                                    int y_type, unsigned int flags, void* stream) {
+  if (y_type != SPENSE_TYPE_BF16 && y_type != SPENSE_TYPE_F32) return fail(SPENSE_ERR_ARG, "unknown y_type %d", y_type);
+  if (flags & ~static_cast<unsigned int>(SPENSE_MX4_SCALE_ROWS))
+    return fail(SPENSE_ERR_ARG, "unknown flags 0x%x", flags);
+  spense_status st = check_mx4_types(M, K);
+  if (st != SPENSE_OK) return st;
+  if (M > 0 && (Xq == nullptr || x_scale == nullptr || Y == nullptr))
+    return fail(SPENSE_ERR_ARG, "Xq, x_scale or Y is NULL");
+  if (!aligned(Xq, 16) || !aligned(x_scale, 16) || !aligned(Y, 16))
+    return fail(SPENSE_ERR_ALIGN, "Xq, x_scale and Y must be 16-byte aligned");
+  int dev = 0;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != SPENSE_OK) return st;
+  const cudaError_t e = launch_mx4_dequantize(Xq, x_scale, (flags & SPENSE_MX4_SCALE_ROWS) == 0, M, K, Y, y_type,
+                                              info.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mx4 dequantize launch");
+  return ok();
+}
+
+spense_status spense_mx4_pack(const uint8_t* Wq, const uint8_t* w_scale, int64_t E, int64_t N, int64_t K,
+                              void* stream_v, spense_mx4_packed** out) {
+  if (out == nullptr) return fail(SPENSE_ERR_ARG, "out is NULL");
+  *out = nullptr;
+  if (Wq == nullptr || w_scale == nullptr) return fail(SPENSE_ERR_ARG, "Wq or w_scale is NULL");
+  if (E < 1 || E > kMx4MaxExperts)
+    return fail(SPENSE_ERR_SHAPE, "%lld experts outside [1, %d]", (long long)E, kMx4MaxExperts);
+  if (N < 1 || N > (1 << 20)) return fail(SPENSE_ERR_SHAPE, "N = %lld outside [1, 2^20]", (long long)N);
+  spense_status st = check_mx4_types(0, K);
+  if (st != SPENSE_OK) return st;
+  const int64_t n_tiles = (N + kMx4Rows - 1) / kMx4Rows, kblocks = (K + kMx4Cols - 1) / kMx4Cols;
+  if (E * n_tiles * kblocks > INT_MAX)
+    return fail(SPENSE_ERR_SHAPE, "too many blocks for one weight (%lld)", (long long)(E * n_tiles * kblocks));
+  if (!aligned(Wq, 16)) return fail(SPENSE_ERR_ALIGN, "Wq is not 16-byte aligned");
+  int dev = 0;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != SPENSE_OK) return st;
+  spense_mx4_packed* h = new (std::nothrow) spense_mx4_packed;
+  if (h == nullptr) return fail(SPENSE_ERR_OOM, "out of host memory");
+  h->device = dev;
+  h->E = E;
+  h->N = N;
+  h->K = K;
+  h->n_tiles = static_cast<int>(n_tiles);
+  h->kblocks = static_cast<int>(kblocks);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  unsigned int* err_d = nullptr;
+  unsigned int err = 0;
+  cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->blocks),
+                             static_cast<size_t>(E * n_tiles * kblocks) * kMx4BlockBytes);
+  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&err_d), sizeof(unsigned int));
+  if (e == cudaSuccess) e = cudaMemsetAsync(err_d, 0, sizeof(unsigned int), stream);
+  if (e == cudaSuccess)
+    e = launch_mx4_pack(Wq, w_scale, E, N, K, h->n_tiles, h->kblocks, h->blocks, err_d, stream);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&err, err_d, sizeof(err), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (err_d != nullptr) cudaFree(err_d);
+  if (e != cudaSuccess || err != 0) {
+    spense_mx4_free(h);
+    if (e != cudaSuccess) return cuda_fail(e, "mx4 pack");
+    return fail(SPENSE_ERR_NONFINITE, "w_scale holds a NaN byte (255)");
+  }
+  *out = h;
+  return ok();
+}
+
+spense_status spense_mx4_free(spense_mx4_packed* Wp) {
+  if (Wp != nullptr) {
+    if (Wp->blocks != nullptr) cudaFree(Wp->blocks);
+    delete Wp;
+  }
+  return ok();
+}
+
+spense_status spense_mx4_get_info(const spense_mx4_packed* Wp, spense_mx4_info* info) {
+  if (Wp == nullptr || info == nullptr) return fail(SPENSE_ERR_ARG, "NULL argument");
+  info->E = Wp->E;
+  info->N = Wp->N;
+  info->K = Wp->K;
+  info->n_tiles = Wp->n_tiles;
+  info->k_blocks = Wp->kblocks;
+  info->blocks = Wp->blocks;
+  info->weight_bytes = static_cast<uint64_t>(Wp->E) * Wp->n_tiles * Wp->kblocks * kMx4BlockBytes;
+  return ok();
+}
+
+size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M) {
+  if (Wp == nullptr || M < 0 || M > kMx4MaxRows) {
+    fail(SPENSE_ERR_ARG, "Wp is NULL or M outside [0, 2^20]");
+    return 0;
+  }
+  return kMx4Workspace;
+}
+
+spense_status spense_mx4_gemm(const spense_mx4_packed* Wp, const uint8_t* Xq, const uint8_t* x_scale, int64_t M,
+                              uint16_t* Y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  if (Wp != nullptr && Wp->E != 1)
+    return fail(SPENSE_ERR_ARG, "the weight holds %lld experts: use spense_mx4_gemm_experts", (long long)Wp->E);
+  return run_mx4(Wp, Xq, x_scale, M, nullptr, Y, ldy, workspace, workspace_bytes, stream);
+}
+
+spense_status spense_mx4_gemm_experts(const spense_mx4_packed* Wp, const uint8_t* Xq, const uint8_t* x_scale,
+                                      int64_t T, const int32_t* offsets, uint16_t* Y, int64_t ldy, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  if (offsets == nullptr) return fail(SPENSE_ERR_ARG, "offsets is NULL");
+  if (!aligned(offsets, 4)) return fail(SPENSE_ERR_ALIGN, "offsets is not 4-byte aligned");
+  return run_mx4(Wp, Xq, x_scale, T, offsets, Y, ldy, workspace, workspace_bytes, stream);
+}
+
+size_t spense_expert_sort_workspace_size(int64_t M, int64_t k, int64_t E) {
+  if (M < 0 || M > kMx4MaxRows || k < 1 || k > 64 || M * k > (1 << 24) || E < 1 || E > kMx4MaxExperts) {
+    fail(SPENSE_ERR_SHAPE, "M = %lld, k = %lld or E = %lld out of range", (long long)M, (long long)k, (long long)E);
+    return 0;
+  }
+  return round_up(static_cast<size_t>(expert_sort_chunks(M * k) * E) * 4, 256);
+}
+
+spense_status spense_expert_sort(const void* ids, int id_bits, int64_t M, int64_t k, int64_t E, int32_t* offsets,
+                                 int32_t* rows, int32_t* pos, void* workspace, size_t workspace_bytes, void* stream) {
+  if (id_bits != 32 && id_bits != 64) return fail(SPENSE_ERR_ARG, "id_bits is %d, not 32 or 64", id_bits);
+  const size_t need = spense_expert_sort_workspace_size(M, k, E);
+  if (need == 0) return SPENSE_ERR_SHAPE;
+  if (offsets == nullptr || (M > 0 && (ids == nullptr || rows == nullptr || pos == nullptr)))
+    return fail(SPENSE_ERR_ARG, "ids, offsets, rows or pos is NULL");
+  if (!aligned(ids, id_bits / 8) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(pos, 4))
+    return fail(SPENSE_ERR_ALIGN, "ids, offsets, rows and pos must be aligned to their type");
+  if (workspace == nullptr) return fail(SPENSE_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(workspace, 256)) return fail(SPENSE_ERR_ALIGN, "workspace is not 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(SPENSE_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", workspace_bytes, need);
+  int dev = 0;
+  DeviceInfo info;
+  const spense_status st = current_device(&dev, &info);
+  if (st != SPENSE_OK) return st;
+  const cudaError_t e = launch_expert_sort(ids, id_bits == 64, M * k, static_cast<int>(k), static_cast<int>(E),
+                                           offsets, rows, pos, static_cast<int32_t*>(workspace),
+                                           static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "expert sort launch");
+  return ok();
+}
+
+spense_status spense_expert_combine(const uint16_t* Y, int64_t T, int64_t N, int64_t ldy, const int32_t* pos,
+                                    const float* weights, int64_t M, int64_t k, uint16_t* out, int64_t ldo,
+                                    void* stream) {
+  if (T < 0 || T > (1 << 24) || M < 0 || M > kMx4MaxRows || k < 1 || k > 64 || N < 1 || N > (1 << 20))
+    return fail(SPENSE_ERR_SHAPE, "T = %lld, M = %lld, k = %lld or N = %lld out of range", (long long)T, (long long)M,
+                (long long)k, (long long)N);
+  if (ldy < N || ldy > (1 << 30) || ldo < N || ldo > (1 << 30))
+    return fail(SPENSE_ERR_SHAPE, "ldy = %lld or ldo = %lld outside [N = %lld, 2^30]", (long long)ldy, (long long)ldo,
+                (long long)N);
+  if (M > 0 && ((T > 0 && Y == nullptr) || pos == nullptr || weights == nullptr || out == nullptr))
+    return fail(SPENSE_ERR_ARG, "Y, pos, weights or out is NULL");
+  if (!aligned(Y, 16) || !aligned(out, 16) || !aligned(pos, 4) || !aligned(weights, 4))
+    return fail(SPENSE_ERR_ALIGN, "Y and out must be 16-byte aligned, pos and weights 4-byte");
+  int dev = 0;
+  DeviceInfo info;
+  const spense_status st = current_device(&dev, &info);
+  if (st != SPENSE_OK) return st;
+  const cudaError_t e = launch_expert_combine(Y, T, N, ldy, pos, weights, M, static_cast<int>(k), out, ldo,
+                                              static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "expert combine launch");
+  return ok();
+}
+
+}  // extern "C"

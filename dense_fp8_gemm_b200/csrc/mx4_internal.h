@@ -1,0 +1,66 @@
+// Internal declarations of the MXFP4 and expert operators. Not part of the
+// public ABI.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace spense {
+
+// A packed MXFP4 weight block: 128 rows x 256 columns. Codes first, 128 bytes a
+// row in the 128-byte swizzle, then the scales of the block's two column groups
+// of 128: 32 lanes x 4 words, word w of lane l the four scale bytes of row
+// 32 w + l (the order tcgen05.cp moves into tensor memory).
+constexpr int kMx4Rows = 128;
+constexpr int kMx4Cols = 256;
+constexpr int kMx4CodeBytes = 16384;
+constexpr int kMx4ScaleBytes = 1024;
+constexpr int kMx4BlockBytes = kMx4CodeBytes + kMx4ScaleBytes;
+
+constexpr int kMx4MaxExperts = 1024;
+constexpr int64_t kMx4MaxRows = 1 << 20;
+
+struct Mx4GemmParams {
+  const uint8_t* blocks;
+  const uint32_t* xs;      // activation scale words [groups][T]
+  uint16_t* y;
+  int64_t ldy;
+  const int32_t* offsets;  // device int32 [E + 1], or NULL: one expert with all T rows
+  unsigned int* status;
+  const unsigned int* test_gate;  // test build only: loaders wait (bounded) until this word is nonzero
+  int E, N, T;
+  int n_tiles, kblocks, groups;
+  int last_steps;          // K = 64 steps in the last block (1 .. 4)
+  int npad;                // rows of activations per tile (MMA N), a multiple of 16
+  int box[3];              // rows one activation load covers, smallest first; box[2] == npad
+  int stages, nacc;
+  int split;               // CTAs of a cluster sharing one tile's K range (1: none)
+  uint32_t stage_bytes, xs_off, recv_bytes, tmem_cols;
+  int w_keep;              // 1: weights are read again by later tiles, keep them in L2
+};
+
+struct Mx4GemmPlan {
+  int npad, stages, nacc, split, ctas_per_sm, grid;
+  uint32_t stage_bytes, xs_off, recv_bytes, tmem_cols, smem_bytes;
+};
+
+cudaError_t launch_mx4_gemm(const CUtensorMap (&maps)[3], const Mx4GemmParams& p, int grid, uint32_t smem_bytes,
+                            cudaStream_t stream);
+
+// x_type: SPENSE_TYPE_*. rows: gather index [T] or NULL. words: scales as words.
+cudaError_t launch_mx4_quantize(const void* X, int x_type, int64_t T, int64_t K, int64_t ldx, const int32_t* rows,
+                                int64_t M_src, uint8_t* Xq, uint8_t* xs, bool words, int sms, cudaStream_t stream);
+cudaError_t launch_mx4_dequantize(const uint8_t* Xq, const uint8_t* xs, bool words, int64_t T, int64_t K, void* Y,
+                                  int y_type, int sms, cudaStream_t stream);
+cudaError_t launch_mx4_pack(const uint8_t* Wq, const uint8_t* ws, int64_t E, int64_t N, int64_t K, int n_tiles,
+                            int kblocks, uint8_t* blocks, unsigned int* err, cudaStream_t stream);
+
+int64_t expert_sort_chunks(int64_t n);
+cudaError_t launch_expert_sort(const void* ids, bool wide, int64_t n, int k, int E, int32_t* offsets, int32_t* rows,
+                               int32_t* pos, int32_t* counts, cudaStream_t stream);
+cudaError_t launch_expert_combine(const uint16_t* Y, int64_t T, int64_t N, int64_t ldy, const int32_t* pos,
+                                  const float* weights, int64_t M, int k, uint16_t* out, int64_t ldo,
+                                  cudaStream_t stream);
+
+}  // namespace spense

@@ -15,6 +15,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "abi_util.h"
 #include "spense_internal.h"
 
 using namespace spense;
@@ -36,8 +37,10 @@ struct spense_packed {
 };
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+namespace spense {
 
 spense_status fail(spense_status code, const char* fmt, ...) {
   char buf[512];
@@ -59,15 +62,6 @@ spense_status cuda_fail(cudaError_t e, const char* what) {
     return fail(SPENSE_ERR_OOM, "%s: %s", what, cudaGetErrorString(e));
   return fail(SPENSE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-struct DeviceInfo {
-  int major = 0;
-  int sms = 0;
-};
 
 // Current device's capability and SM count (cached per device).
 spense_status current_device(int* dev, DeviceInfo* info) {
@@ -104,6 +98,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+}  // namespace spense
+
+namespace {
 
 void free_handle(spense_packed* h) {
   if (h == nullptr) return;

@@ -32,12 +32,19 @@ SYMBOLS = (
     "spense_quantize", "spense_score_glu", "spense_score_workspace_size", "spense_select_dense",
     "spense_pack_rows", "spense_plan_shapes", "spense_gemm_grouped_host",
     "spense_gemm_grouped_host_workspace_size", "spense_glu_order", "spense_noalloc_status",
+    "spense_mx4_quantize", "spense_mx4_dequantize", "spense_mx4_pack", "spense_mx4_free", "spense_mx4_get_info",
+    "spense_mx4_workspace_size", "spense_mx4_gemm", "spense_mx4_gemm_experts", "spense_expert_sort",
+    "spense_expert_sort_workspace_size", "spense_expert_combine",
 )
 GEMM_X_PACKED_ORDER = 1
 GEMM_HOST_X = 2
 GEMM_HOST_Y = 4
 MAX_GROUP = 4
 NOALLOC_SCRATCH_BYTES = (8 << 20) + (64 << 10)
+
+
+MX4_SCALE_ROWS = 1
+MX4_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class SpenseError(RuntimeError):
@@ -54,6 +61,11 @@ class PackedInfo(ctypes.Structure):
         ("w_scale", ctypes.c_void_p), ("Vs", ctypes.c_void_p), ("E", ctypes.c_void_p),
         ("Wd", ctypes.c_void_p), ("perm", ctypes.c_void_p), ("weight_bytes", ctypes.c_uint64),
     ]
+
+
+class Mx4Info(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("n_tiles", ctypes.c_int64),
+                ("k_blocks", ctypes.c_int64), ("blocks", ctypes.c_void_p), ("weight_bytes", ctypes.c_uint64)]
 
 
 _lib = None
@@ -115,6 +127,20 @@ def lib() -> ctypes.CDLL:
     L.spense_gemm_grouped_host_workspace_size.restype = SZ
     L.spense_glu_order.argtypes = [I64, P, I64, P]
     L.spense_noalloc_status.argtypes = [P, ctypes.POINTER(U32)]
+    I = ctypes.c_int
+    L.spense_mx4_quantize.argtypes = [P, I, I64, I64, I64, P, I64, P, P, U32, P]
+    L.spense_mx4_dequantize.argtypes = [P, P, I64, I64, P, I, U32, P]
+    L.spense_mx4_pack.argtypes = [P, P, I64, I64, I64, P, ctypes.POINTER(P)]
+    L.spense_mx4_free.argtypes = [P]
+    L.spense_mx4_get_info.argtypes = [P, ctypes.POINTER(Mx4Info)]
+    L.spense_mx4_workspace_size.argtypes = [P, I64]
+    L.spense_mx4_workspace_size.restype = SZ
+    L.spense_mx4_gemm.argtypes = [P, P, P, I64, P, I64, P, SZ, P]
+    L.spense_mx4_gemm_experts.argtypes = [P, P, P, I64, P, P, I64, P, SZ, P]
+    L.spense_expert_sort.argtypes = [P, I, I64, I64, I64, P, P, P, P, SZ, P]
+    L.spense_expert_sort_workspace_size.argtypes = [I64, I64, I64]
+    L.spense_expert_sort_workspace_size.restype = SZ
+    L.spense_expert_combine.argtypes = [P, I64, I64, I64, P, P, I64, I64, P, I64, P]
     L.spense_last_error.restype = ctypes.c_char_p
     L.spense_version.restype = ctypes.c_char_p
     for name in ("spense_pack", "spense_gemm", "spense_gemm_host", "spense_free", "spense_get_info",
@@ -529,4 +555,267 @@ def select_dense(score: torch.Tensor, Kd: int, out: torch.Tensor | None = None, 
     code = lib().spense_select_dense(_dev_ptr(score, torch.float32, "score"), I, int(Kd),
                                      _dev_ptr(out, torch.int32, "dense_idx") if Kd > 0 else None, _stream(stream))
     _check(code, "spense_select_dense")
+    return out
+
+
+def _current(name: str, *tensors):
+    """The device of `tensors`, which has to be the current one: the library
+    launches there, and addresses of another device mean nothing on it."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _row_strided(t: torch.Tensor, name: str):
+    """Address and row stride of a 2-D CUDA tensor with unit column stride (a
+    column slice of a wider one may be given; rows may not overlap)."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.data_ptr(), ld
+
+
+def _scale_flags(x_scale: torch.Tensor, M: int, K: int) -> int:
+    """MX4_SCALE_ROWS for scales [M, K / 32], 0 for words [ceil(K / 128), M, 4]."""
+    if x_scale.shape == (-(-K // 128), M, 4):
+        return 0
+    if x_scale.shape == (M, K // 32):
+        return MX4_SCALE_ROWS
+    raise ValueError(f"scales of {M} rows of {K} columns are [{-(-K // 128)}, {M}, 4] words or [{M}, {K // 32}] rows, "
+                     f"got {tuple(x_scale.shape)}")
+
+
+def mx4_quantize(X: torch.Tensor, rows: torch.Tensor | None = None, scale_rows: bool = False,
+                 Xq: torch.Tensor | None = None, x_scale: torch.Tensor | None = None, stream=None):
+    """spense_mx4_quantize: MXFP4 of X [M, K] (bfloat16, float16 or float32; rows
+    may be strided), or of the rows X[rows] with an int32 index tensor (entries
+    outside [0, M) leave their output row as it was). Returns (Xq uint8
+    [T, K / 2], x_scale uint8): scales as words [ceil(K / 128), T, 4], or
+    [T, K / 32] with scale_rows (the layout mx4_pack takes)."""
+    if X.dtype not in MX4_TYPES:
+        raise TypeError(f"X must be bfloat16, float16 or float32, got {X.dtype}")
+    ptr, ldx = _row_strided(X, "X")
+    M, K = X.shape
+    T = M if rows is None else rows.shape[0]
+    if Xq is None:
+        Xq = torch.empty((T, K // 2), dtype=torch.uint8, device=X.device)
+    if x_scale is None:
+        x_scale = torch.empty((T, K // 32) if scale_rows else (-(-K // 128), T, 4), dtype=torch.uint8, device=X.device)
+    if Xq.shape != (T, K // 2):
+        raise ValueError(f"Xq must be [{T}, {K // 2}], got {tuple(Xq.shape)}")
+    if rows is not None and rows.dim() != 1:
+        raise ValueError("rows must be 1-D")
+    flags = MX4_SCALE_ROWS if scale_rows else _scale_flags(x_scale, T, K)
+    if scale_rows and x_scale.shape != (T, K // 32):
+        raise ValueError(f"x_scale must be [{T}, {K // 32}], got {tuple(x_scale.shape)}")
+    _current("mx4_quantize", X, rows, Xq, x_scale)
+    code = lib().spense_mx4_quantize(ptr, MX4_TYPES[X.dtype], M, K, ldx, _dev_ptr(rows, torch.int32, "rows"), T,
+                                     _dev_ptr(Xq, torch.uint8, "Xq"), _dev_ptr(x_scale, torch.uint8, "x_scale"),
+                                     flags, _stream(stream))
+    _check(code, "spense_mx4_quantize")
+    return Xq, x_scale
+
+
+def mx4_dequantize(Xq: torch.Tensor, x_scale: torch.Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """spense_mx4_dequantize: the values [M, K] of codes [M, K / 2] and their scales
+    (either layout), as bfloat16 or float32."""
+    M, K = Xq.shape[0], Xq.shape[1] * 2
+    if out is None:
+        out = torch.empty((M, K), dtype=dtype, device=Xq.device)
+    if out.shape != (M, K) or out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"the output must be bfloat16 or float32 [{M}, {K}], got {out.dtype} {tuple(out.shape)}")
+    flags = _scale_flags(x_scale, M, K)
+    _current("mx4_dequantize", Xq, x_scale, out)
+    code = lib().spense_mx4_dequantize(_dev_ptr(Xq, torch.uint8, "Xq"), _dev_ptr(x_scale, torch.uint8, "x_scale"), M,
+                                       K, _dev_ptr(out, out.dtype, "out"), MX4_TYPES[out.dtype], flags,
+                                       _stream(stream))
+    _check(code, "spense_mx4_dequantize")
+    return out
+
+
+class Mx4Weight:
+    """A packed MXFP4 weight, or one per expert (owns its device buffer through the C handle)."""
+
+    def __init__(self, handle: ctypes.c_void_p):
+        self._h = handle
+        self.info = Mx4Info()
+        _check(lib().spense_mx4_get_info(self._h, ctypes.byref(self.info)), "spense_mx4_get_info")
+
+    @property
+    def handle(self):
+        return self._h
+
+    @property
+    def E(self):
+        return self.info.E
+
+    @property
+    def N(self):
+        return self.info.N
+
+    @property
+    def K(self):
+        return self.info.K
+
+    @property
+    def weight_bytes(self):
+        return int(self.info.weight_bytes)
+
+    def blocks(self) -> torch.Tensor:
+        """Read-only view of the packed blocks, uint8 [E, n_tiles, k_blocks, 17408]."""
+        i = self.info
+        return torch.as_tensor(_DevView(i.blocks, (i.E, i.n_tiles, i.k_blocks, 17408), "|u1"), device="cuda")
+
+    def free(self):
+        if self._h is not None and self._h.value:
+            _check(lib().spense_mx4_free(self._h), "spense_mx4_free")
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def mx4_pack(Wq: torch.Tensor, w_scale: torch.Tensor, stream=None) -> Mx4Weight:
+    """spense_mx4_pack: codes [N, K / 2] and scale bytes [N, K / 32] of a weight, or
+    [E, N, K / 2] and [E, N, K / 32] of one weight per expert."""
+    if Wq.dim() not in (2, 3) or w_scale.shape != (*Wq.shape[:-1], Wq.shape[-1] // 16):
+        raise ValueError(f"codes [.., N, K / 2] and scales [.., N, K / 32] expected, got {tuple(Wq.shape)} and "
+                         f"{tuple(w_scale.shape)}")
+    E, (N, K) = (Wq.shape[0] if Wq.dim() == 3 else 1), (Wq.shape[-2], Wq.shape[-1] * 2)
+    _current("mx4_pack", Wq, w_scale)
+    out = ctypes.c_void_p()
+    code = lib().spense_mx4_pack(_dev_ptr(Wq, torch.uint8, "Wq"), _dev_ptr(w_scale, torch.uint8, "w_scale"), E, N, K,
+                                 _stream(stream), ctypes.byref(out))
+    _check(code, "spense_mx4_pack")
+    return Mx4Weight(out)
+
+
+def mx4_workspace_size(pw: Mx4Weight, M: int) -> int:
+    n = lib().spense_mx4_workspace_size(pw.handle, M)
+    if n == 0:
+        _check(1, "spense_mx4_workspace_size")
+    return int(n)
+
+
+class PreparedMx4Gemm:
+    """spense_mx4_gemm, or with offsets spense_mx4_gemm_experts, with its arguments
+    marshalled once (for loops that launch the same product on the same buffers):
+    calling it makes one C call. The tensors must stay alive and in place."""
+
+    def __init__(self, pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, Y: torch.Tensor,
+                 workspace: torch.Tensor, offsets: torch.Tensor | None = None):
+        M, K = Xq.shape[0], pw.K
+        if Xq.dim() != 2 or Xq.shape[1] * 2 != K:
+            raise ValueError(f"Xq must be [M, {K // 2}], got {tuple(Xq.shape)}")
+        if _scale_flags(x_scale, M, K) != 0 and M > 0:
+            raise ValueError("the products take activation scales as words, not rows")
+        if Y.dtype != torch.bfloat16 or Y.shape != (M, pw.N):
+            raise ValueError(f"Y must be bfloat16 [{M}, {pw.N}], got {Y.dtype} {tuple(Y.shape)}")
+        if offsets is not None and offsets.shape != (pw.E + 1,):
+            raise ValueError(f"offsets must be [{pw.E + 1}], got {tuple(offsets.shape)}")
+        _current("mx4_gemm", Xq, x_scale, Y, workspace, offsets)
+        y, ldy = _row_strided(Y, "Y")
+        self._keep = (pw, Xq, x_scale, Y, workspace, offsets)
+        self._where = "spense_mx4_gemm" if offsets is None else "spense_mx4_gemm_experts"
+        self._fn = getattr(lib(), self._where)
+        args = [pw.handle, _dev_ptr(Xq, torch.uint8, "Xq"), _dev_ptr(x_scale, torch.uint8, "x_scale"), M]
+        if offsets is not None:
+            args.append(_dev_ptr(offsets, torch.int32, "offsets"))
+        self._args = (*args, ctypes.c_void_p(y), max(ldy, pw.N), _dev_ptr(workspace, torch.uint8, "workspace"),
+                      workspace.numel())
+
+    def __call__(self, stream=None):
+        code = self._fn(*self._args, _stream(stream))
+        if code != SPENSE_OK:
+            _check(code, self._where)
+
+
+def mx4_gemm(pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, Y: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """spense_mx4_gemm: Y [M, N] bf16 = X x W^T of MXFP4 activations (mx4_quantize) and
+    a packed weight. Y may be a column slice of a wider tensor."""
+    if Y is None:
+        Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
+    if workspace is None:
+        workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
+    PreparedMx4Gemm(pw, Xq, x_scale, Y, workspace)(stream)
+    return Y
+
+
+def mx4_gemm_experts(pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, offsets: torch.Tensor,
+                     Y: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """spense_mx4_gemm_experts: rows offsets[e] .. offsets[e + 1] (device int32
+    [E + 1]) of X with expert e's weight. Rows outside every range are left as
+    they were in Y (unset in a Y made here)."""
+    if Y is None:
+        Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
+    if workspace is None:
+        workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
+    PreparedMx4Gemm(pw, Xq, x_scale, Y, workspace, offsets)(stream)
+    return Y
+
+
+def expert_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None,
+                pos: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """spense_expert_sort: choices ids [M, k] (int32 or int64; outside [0, E): left
+    out) sorted by expert, stably. Returns (offsets int32 [E + 1], rows int32
+    [M k]: the token of every slot, -1 behind the last; pos int32 [M, k]: the slot
+    of every choice, -1 for one left out)."""
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64 [M, k], got {ids.dtype} {tuple(ids.shape)}")
+    M, k = ids.shape
+    dev = ids.device
+    if offsets is None:
+        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    if rows is None:
+        rows = torch.empty((M * k,), dtype=torch.int32, device=dev)
+    if pos is None:
+        pos = torch.empty((M, k), dtype=torch.int32, device=dev)
+    if offsets.shape != (E + 1,) or rows.shape != (M * k,) or pos.shape != (M, k):
+        raise ValueError(f"offsets [{E + 1}], rows [{M * k}] and pos [{M}, {k}] expected")
+    if workspace is None:
+        need = int(lib().spense_expert_sort_workspace_size(M, k, E))
+        if need == 0:
+            _check(2, "spense_expert_sort")
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    _current("expert_sort", ids, offsets, rows, pos, workspace)
+    code = lib().spense_expert_sort(_dev_ptr(ids, ids.dtype, "ids"), 32 if ids.dtype == torch.int32 else 64, M, k, E,
+                                    _dev_ptr(offsets, torch.int32, "offsets"), _dev_ptr(rows, torch.int32, "rows"),
+                                    _dev_ptr(pos, torch.int32, "pos"), _dev_ptr(workspace, torch.uint8, "workspace"),
+                                    workspace.numel(), _stream(stream))
+    _check(code, "spense_expert_sort")
+    return offsets, rows, pos
+
+
+def expert_combine(Y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """spense_expert_combine: out[m] = sum_j weights[m, j] Y[pos[m, j]] in fp32, rounded
+    to bf16; choices with pos outside Y's rows are left out. Y and out may be
+    column slices of wider tensors."""
+    if Y.dtype != torch.bfloat16:
+        raise TypeError(f"Y must be bfloat16, got {Y.dtype}")
+    y, ldy = _row_strided(Y, "Y")
+    T, N = Y.shape
+    if pos.dim() != 2 or weights.shape != pos.shape:
+        raise ValueError(f"pos and weights must be [M, k], got {tuple(pos.shape)} and {tuple(weights.shape)}")
+    M, k = pos.shape
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=Y.device)
+    if out.shape != (M, N) or out.dtype != torch.bfloat16:
+        raise ValueError(f"out must be bfloat16 [{M}, {N}], got {out.dtype} {tuple(out.shape)}")
+    o, ldo = _row_strided(out, "out")
+    _current("expert_combine", Y, pos, weights, out)
+    code = lib().spense_expert_combine(y, T, N, ldy, _dev_ptr(pos, torch.int32, "pos"),
+                                       _dev_ptr(weights, torch.float32, "weights"), M, k, o, ldo, _stream(stream))
+    _check(code, "spense_expert_combine")
     return out

@@ -442,6 +442,166 @@ typedef struct spense_plan_info {
 SPENSE_API spense_status spense_plan_shapes(int count, const int64_t* N, const int64_t* K, const int64_t* Kd,
                                             int64_t M, int sms, spense_plan_info* out);
 
+/*
+ * ------------------------------------------------------------------ MXFP4
+ * Products of 4-bit weights and activations in the OCP Microscaling format
+ * MXFP4, plain and grouped by expert, and what goes before and behind them.
+ * The pages of the Spense method have no counterpart to these calls.
+ *
+ * The format: 32 consecutive columns of a row share one power-of-two scale, a
+ * byte b meaning 2^(b - 127) (255: NaN); each value is an e2m1 code (bit 3 the
+ * sign, codes 0 .. 7 the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6), two codes to a
+ * byte with the even column in the low nibble. A row of K columns is K / 2 code
+ * bytes and K / 32 scale bytes. K is a multiple of 32 in [32, 2^20].
+ *
+ * Scale bytes of R rows come in one of two layouts:
+ *   words (the products' activations; the default)  [ceil(K / 128)][R][4]: the
+ *       four scale bytes of 128 columns of a row together, the words of
+ *       neighbouring rows next to each other. Bytes past K / 32 (in the last
+ *       words when K is no multiple of 128) must not be 255; spense_mx4_quantize
+ *       writes 0.
+ *   rows (the format's own; weights)  [R][K / 32], with SPENSE_MX4_SCALE_ROWS.
+ * At most 2^20 rows a call.
+ */
+enum { SPENSE_TYPE_BF16 = 0, SPENSE_TYPE_F16 = 1, SPENSE_TYPE_F32 = 2 };
+
+/* Flag of spense_mx4_quantize and spense_mx4_dequantize: scales in the rows layout. */
+enum { SPENSE_MX4_SCALE_ROWS = 1u };
+
+/*
+ * spense_mx4_quantize — MXFP4 of T rows, optionally gathered. For a block of 32
+ * columns with largest magnitude a: e = floor(log2 a) - 2, at least -127 (also
+ * for an all-zero block); scale byte e + 127; codes round x 2^-e to the nearest
+ * value, ties to the even code, saturating at 6 (magnitudes above 6 2^e, by less
+ * than 8 / 6). A block with a NaN or an infinity gets scale byte 255 and
+ * unspecified codes (all its values read as NaN).
+ *   X        device, [M][K] values of x_type (SPENSE_TYPE_*), row m at X + m * ldx
+ *            elements; X and ldx * element size multiples of 16 bytes.
+ *   rows     NULL: output row r is row r of X, T == M. Else device int32 [T]:
+ *            output row r is row rows[r] of X (for example the rows array of
+ *            spense_expert_sort). Where rows[r] is outside [0, M) the output row's
+ *            codes and scales are left as they were.
+ *   Xq       device, codes [T][K / 2], 16-byte aligned (caller-owned).
+ *   x_scale  device, scale bytes of the T rows in the words layout, or the rows
+ *            layout with flags = SPENSE_MX4_SCALE_ROWS; 16-byte aligned.
+ * Asynchronous on `stream`. Errors: ARG, SHAPE, ALIGN, UNSUPPORTED, CUDA.
+ */
+SPENSE_API spense_status spense_mx4_quantize(const void* X, int x_type, int64_t M, int64_t K, int64_t ldx,
+                                             const int32_t* rows, int64_t T, uint8_t* Xq, uint8_t* x_scale,
+                                             unsigned int flags, void* stream);
+
+/*
+ * spense_mx4_dequantize — the values of M rows of codes and scales, as bf16 or
+ * fp32 (y_type), contiguous [M][K]. Exact for every scale byte below 253 (6 2^126
+ * and more may round to infinity); scale byte 255 gives NaN.
+ * Asynchronous on `stream`. Errors: ARG, SHAPE, ALIGN, UNSUPPORTED, CUDA.
+ */
+SPENSE_API spense_status spense_mx4_dequantize(const uint8_t* Xq, const uint8_t* x_scale, int64_t M, int64_t K,
+                                               void* Y, int y_type, unsigned int flags, void* stream);
+
+/* Opaque packed MXFP4 weight (one matrix, or one per expert). Owns its device buffer. */
+typedef struct spense_mx4_packed spense_mx4_packed;
+
+/*
+ * spense_mx4_pack — E weight matrices [N][K] into the layout the products
+ * stream: per 128 rows and 256 columns one block of 17408 bytes (codes in the
+ * tensor cores' swizzle, then the scales in the order they are read), rows and
+ * columns padded with zeros.
+ *   Wq       device, codes [E][N][K / 2], 16-byte aligned. Read only.
+ *   w_scale  device, scale bytes [E][N][K / 32] (rows layout), none of them 255.
+ *   E        1 .. 1024 (1: a plain weight).   N  1 .. 2^20.
+ * Synchronizes `stream`. Errors: ARG, SHAPE, ALIGN, NONFINITE (a scale byte 255),
+ * OOM, CUDA, UNSUPPORTED.
+ */
+SPENSE_API spense_status spense_mx4_pack(const uint8_t* Wq, const uint8_t* w_scale, int64_t E, int64_t N, int64_t K,
+                                         void* stream, spense_mx4_packed** out);
+
+/* Releases the handle and its device buffer (no product using it may be running). NULL is accepted. */
+SPENSE_API spense_status spense_mx4_free(spense_mx4_packed* Wp);
+
+typedef struct spense_mx4_info {
+  int64_t E, N, K;
+  int64_t n_tiles, k_blocks;  /* 128-row tiles, 256-column blocks of one matrix */
+  const void* blocks;         /* device [E][n_tiles][k_blocks][17408] */
+  uint64_t weight_bytes;
+} spense_mx4_info;
+
+SPENSE_API spense_status spense_mx4_get_info(const spense_mx4_packed* Wp, spense_mx4_info* info);
+
+/* Bytes of workspace the MXFP4 products need for M rows; 0 on a bad argument. */
+SPENSE_API size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M);
+
+/*
+ * spense_mx4_gemm — Y[m][n] = bf16(sum_k X[m][k] W[n][k]) of MXFP4 activations and
+ * a packed MXFP4 weight with E = 1; products and sums in fp32 (a fixed order:
+ * repeatable bit for bit).
+ *   Xq, x_scale  device, codes [M][K / 2] and scale bytes in the words layout,
+ *                16-byte aligned, as spense_mx4_quantize writes them. A scale
+ *                byte 255 makes its row of Y NaN.
+ *   M            0 .. 2^20 rows (0: nothing to do).
+ *   Y            device, bf16, row m at Y + m * ldy, N <= ldy <= 2^30, 16-byte
+ *                aligned (16-byte stores are used when ldy % 8 == 0).
+ *   workspace    at least spense_mx4_workspace_size bytes, 256-byte aligned,
+ *                ZERO-FILLED before its first use, with the rules of spense_gemm;
+ *                spense_workspace_status reads its status word.
+ * Asynchronous on `stream`. Errors: ARG, SHAPE, ALIGN, WORKSPACE, UNSUPPORTED, CUDA.
+ */
+SPENSE_API spense_status spense_mx4_gemm(const spense_mx4_packed* Wp, const uint8_t* Xq, const uint8_t* x_scale,
+                                         int64_t M, uint16_t* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/*
+ * spense_mx4_gemm_experts — the same product grouped by expert: for every expert
+ * e, rows offsets[e] .. offsets[e + 1] of X with weight e.
+ *   T        rows of X, x_scale (its layout's R) and Y.
+ *   offsets  device int32 [E + 1], ascending, within [0, T] (others are cut to
+ *            that; read on the device only, so nothing is synchronized). An
+ *            expert may have no rows.
+ * Rows outside every expert's range (behind offsets[E], say) are left as they
+ * were in Y. Other arguments and errors as spense_mx4_gemm.
+ */
+SPENSE_API spense_status spense_mx4_gemm_experts(const spense_mx4_packed* Wp, const uint8_t* Xq,
+                                                 const uint8_t* x_scale, int64_t T, const int32_t* offsets,
+                                                 uint16_t* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                                 void* stream);
+
+/*
+ * spense_expert_sort — the choices of M tokens, k experts each, sorted by expert.
+ * A choice whose id is outside [0, E) is left out (a padded token, a dropped
+ * choice, another device's expert). The order is stable: within an expert,
+ * choices keep the order of ids.
+ *   ids      device int32 or int64 (id_bits 32 or 64) [M][k].
+ *   M, k, E  0 <= M <= 2^20, 1 <= k <= 64, M k <= 2^24, 1 <= E <= 1024.
+ *   offsets  device int32 [E + 1]: expert e's choices are the sorted slots
+ *            offsets[e] .. offsets[e + 1].
+ *   rows     device int32 [M k]: the token of every sorted slot; -1 behind offsets[E].
+ *   pos      device int32 [M][k]: the slot of every choice, -1 for one left out.
+ *   workspace  device, 256-byte aligned, at least
+ *            spense_expert_sort_workspace_size(M, k, E) bytes (no zeroing needed;
+ *            not shared by calls that can run at the same time).
+ * Asynchronous on `stream`. Errors: ARG, SHAPE, ALIGN, WORKSPACE, UNSUPPORTED, CUDA.
+ */
+SPENSE_API spense_status spense_expert_sort(const void* ids, int id_bits, int64_t M, int64_t k, int64_t E,
+                                            int32_t* offsets, int32_t* rows, int32_t* pos, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/* Workspace bytes spense_expert_sort needs (0 for a bad shape). */
+SPENSE_API size_t spense_expert_sort_workspace_size(int64_t M, int64_t k, int64_t E);
+
+/*
+ * spense_expert_combine — out[m][n] = bf16(sum_j weights[m][j] Y[pos[m][j]][n]),
+ * summed in fp32 with j ascending. A choice with pos outside [0, T) is left out,
+ * whatever its weight holds; a token without any gets zeros.
+ *   Y        device, bf16, T rows (T <= 2^24), row r at Y + r * ldy, 16-byte aligned.
+ *   pos      device int32 [M][k] (spense_expert_sort);  weights  device fp32 [M][k].
+ *   out      device, bf16, row m at out + m * ldo, 16-byte aligned; must not overlap Y.
+ *   M, k, N  0 <= M <= 2^20, 1 <= k <= 64, 1 <= N <= 2^20;  N <= ldy, ldo <= 2^30.
+ * Asynchronous on `stream`. Errors: ARG, SHAPE, ALIGN, UNSUPPORTED, CUDA.
+ */
+SPENSE_API spense_status spense_expert_combine(const uint16_t* Y, int64_t T, int64_t N, int64_t ldy,
+                                               const int32_t* pos, const float* weights, int64_t M, int64_t k,
+                                               uint16_t* out, int64_t ldo, void* stream);
+
 /* Reads and clears the status word a workspace carries. *status_out receives 0
  * when every kernel that used the workspace completed normally, else a bitwise
  * OR of SPENSE_DEVICE_* codes. Synchronizes `stream`. */
