@@ -28,8 +28,8 @@ constexpr size_t kMx4Workspace = 256;  // the header: status word
 // twice the average, since a heavier expert only costs a second reading of its
 // weights (from L2) and smaller tiles leave a deeper ring.
 //
-// Few tiles: the largest cluster of 8, 4 or 2 that two CTAs a SM can hold at
-// once, that leaves each CTA two blocks or more and room for its ring.
+// Few tiles: the largest cluster (8 CTAs at most) that two CTAs a SM can hold at
+// once, that leaves each CTA two blocks or more, and whose partials fit the ring.
 spense_status make_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, Mx4GemmPlan* out) {
   Mx4GemmPlan pl{};
   const int64_t want = ragged ? std::max<int64_t>(2 * ((T + E - 1) / E), 32) : T;
@@ -40,31 +40,30 @@ spense_status make_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool
   const uint32_t atoms = (static_cast<uint32_t>(pl.npad) + 127u) / 128u;
   pl.xs_off = kMx4BlockBytes + static_cast<uint32_t>(pl.npad) * 128u;
   pl.stage_bytes = pl.xs_off + atoms * 1024u;
-  const uint32_t tail = static_cast<uint32_t>(round_up(256 + 4 * (3 * static_cast<size_t>(E) + 1), 16));
-  // Ring stages beside `recv` bytes of partials with `cps` CTAs a SM.
-  auto ring = [&](int cps, uint32_t recv) {
-    const uint32_t budget = cps == 2 ? 115200u : 232448u, fixed = 1024 + tail + recv;
-    return budget <= fixed ? 0 : static_cast<int>(std::min<uint32_t>(12, (budget - fixed) / pl.stage_bytes));
+  const uint32_t tail = static_cast<uint32_t>(round_up(kMx4BarrierBytes + 4 * (3 * static_cast<size_t>(E) + 1), 16));
+  // Ring stages with `cps` CTAs a SM.
+  auto ring = [&](int cps) {
+    const uint32_t budget = cps == 2 ? 115200u : 232448u, fixed = 1024 + tail;
+    return static_cast<int>(std::min<uint32_t>(12, (budget - fixed) / pl.stage_bytes));
   };
   pl.split = 1;
   pl.ctas_per_sm = 1;
   if (pl.npad <= 64 && tiles < sms)
-    for (int s = 8; s > 1 && pl.split == 1; s >>= 1) {
+    for (int s = 8; s > 1 && pl.split == 1; --s) {
       const int cps = tiles * s > sms ? 2 : 1;
-      const int need = std::max(3, std::min(4, (kblocks + s - 1) / s));
-      if (tiles * s <= 2 * sms && kblocks >= 2 * s && ring(cps, static_cast<uint32_t>((s - 1) * pl.npad * 512)) >= need) {
+      if (tiles * s <= 2 * sms && kblocks >= 2 * s && ring(cps) >= 3 &&
+          static_cast<uint32_t>((s - 1) * pl.npad * 512) <= static_cast<uint32_t>(ring(cps)) * pl.stage_bytes) {
         pl.split = s;
         pl.ctas_per_sm = cps;
       }
     }
-  pl.recv_bytes = static_cast<uint32_t>((pl.split - 1) * pl.npad * 512);
   pl.grid = static_cast<int>(pl.split > 1 ? tiles * pl.split : std::min<int64_t>(tiles, sms));
   pl.nacc = pl.split == 1 && 2 * pl.npad + 48 <= 512 ? 2 : 1;
   pl.tmem_cols = 32;
   while (pl.tmem_cols < static_cast<uint32_t>(pl.nacc * pl.npad + 48)) pl.tmem_cols <<= 1;
-  pl.stages = ring(pl.ctas_per_sm, pl.recv_bytes);
+  pl.stages = ring(pl.ctas_per_sm);
   if (pl.stages < 3) return fail(SPENSE_ERR_SHAPE, "no launch plan for %lld experts", (long long)E);
-  pl.smem_bytes = 1024 + tail + pl.recv_bytes + static_cast<uint32_t>(pl.stages) * pl.stage_bytes;
+  pl.smem_bytes = 1024 + tail + static_cast<uint32_t>(pl.stages) * pl.stage_bytes;
   // A CTA that takes more than half of the tensor memory has the SM to itself.
   if (pl.tmem_cols > 256) pl.smem_bytes = std::max<uint32_t>(pl.smem_bytes, 122880u);
   *out = pl;
@@ -147,7 +146,6 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
   p.split = pl.split;
   p.stage_bytes = pl.stage_bytes;
   p.xs_off = pl.xs_off;
-  p.recv_bytes = pl.recv_bytes;
   p.tmem_cols = pl.tmem_cols;
   p.w_keep = T > pl.npad ? 1 : 0;
   const cudaError_t e = launch_mx4_gemm(maps, p, pl.grid, pl.smem_bytes, static_cast<cudaStream_t>(stream));

@@ -11,7 +11,7 @@
 // device only) and takes every gridDim-th tile, rows of one weight tile next to
 // each other so that the weights' second read hits L2.
 //
-// Roles (288 threads):
+// Roles (320 threads):
 //   warps 0-3 epilogue: tensor memory -> registers -> bf16 rows of Y;
 //   warp 4    one lane copies the scales into tensor memory (tcgen05.cp) and
 //             issues four K = 64 MMAs a block;
@@ -20,10 +20,10 @@
 //             issuing thread's copies one after another;
 //   warp 7    TMA loads of the activation codes, in the smallest of three box
 //             heights that covers the tile's rows;
-//   warp 8    the activation scales: one word (128 columns) a row, put into the
-//             order tcgen05.cp reads (lane l, word w: row 32 w + l) with 4-byte
-//             asynchronous copies, which are coalesced because the words of
-//             neighbouring rows are neighbours in memory.
+//   warps 8,9 the activation scales: one word (128 columns) a row. Warp 8 brings
+//             them in with 4-byte asynchronous copies (coalesced, since the words
+//             of neighbouring rows are neighbours in memory), warp 9 puts them
+//             into the order tcgen05.cp reads (lane l, word w: row 32 w + l).
 //
 // Few tiles (p.split > 1): the CTAs of a cluster split a tile's K range; the
 // peers store their fp32 partials into rank 0's shared memory and rank 0 adds
@@ -43,18 +43,18 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 1500000000ull;
 constexpr int kMaxMx4Stages = 12;
-constexpr int kMx4Threads = 288;
-constexpr int kXsDepth = 3;  // scale copies in flight (at most the number of stages)
+constexpr int kMx4Threads = 320;
 
 struct alignas(16) Mx4Barriers {
   uint64_t full[kMaxMx4Stages];
   uint64_t empty[kMaxMx4Stages];
+  uint64_t xs_in[kMaxMx4Stages];  // a stage's activation scales have landed, in row order
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(Mx4Barriers) <= 256, "barrier area too small");
+static_assert(sizeof(Mx4Barriers) <= kMx4BarrierBytes, "barrier area too small");
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned int* status, unsigned int code,
                                          volatile int* abort_flag) {
@@ -72,6 +72,12 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned
       }
     }
   }
+}
+
+// The same by a whole (converged) warp, which takes one decision.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, unsigned int* status, unsigned int code,
+                                         volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, code, abort_flag));
 }
 
 // The tile list. tile_begin[e] .. tile_begin[e + 1]: expert e's tiles, its row
@@ -93,7 +99,8 @@ struct TileWalker {
   const TileList& list;
   int e;
   __device__ TileWalker(const Mx4GemmParams& pp, const TileList& l) : p(pp), list(l), e(0) {}
-  // Tiles are asked for in ascending order.
+  // Tiles are asked for in ascending order, by whole warps (the values pass
+  // through a shuffle so that the compiler knows them to be uniform).
   __device__ Tile get(int t) {
     while (t >= list.tile_begin[e + 1]) ++e;
     const int local = t - list.tile_begin[e];
@@ -101,7 +108,8 @@ struct TileWalker {
     const int m_tiles = (cnt + p.npad - 1) / p.npad;
     const int nt = local / m_tiles;
     const int r = (local - nt * m_tiles) * p.npad;
-    return Tile{e, nt, list.first[e] + r, min(p.npad, cnt - r)};
+    return Tile{__shfl_sync(0xffffffffu, e, 0), __shfl_sync(0xffffffffu, nt, 0),
+                __shfl_sync(0xffffffffu, list.first[e] + r, 0), __shfl_sync(0xffffffffu, min(p.npad, cnt - r), 0)};
   }
 };
 
@@ -165,16 +173,16 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;  // the swizzled tiles are 1024-byte aligned
-  const uint32_t recv_base = smem_base + static_cast<uint32_t>(p.stages) * p.stage_bytes;
-  uint8_t* const tail = smem_raw + (recv_base - raw) + p.recv_bytes;
+  uint8_t* const tail = smem_raw + (smem_base - raw) + static_cast<uint32_t>(p.stages) * p.stage_bytes;
   Mx4Barriers* const bars = reinterpret_cast<Mx4Barriers*>(tail);
   TileList list;
-  list.tile_begin = reinterpret_cast<int*>(tail + 256);
+  list.tile_begin = reinterpret_cast<int*>(tail + kMx4BarrierBytes);
   list.first = list.tile_begin + p.E + 1;
   list.count = list.first + p.E;
   volatile int* const abort_flag = &bars->abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
+  const int lane = threadIdx.x & 31;
   const uint32_t rank = p.split > 1 ? ptx::cluster_ctarank() : 0u;
   const int unit = static_cast<int>(blockIdx.x) / p.split;  // tiles unit, unit + units, ..
   const int units = static_cast<int>(gridDim.x) / p.split;
@@ -185,6 +193,7 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
     for (int s = 0; s < p.stages; ++s) {
       ptx::mbar_init(ptx::smem_addr(&bars->full[s]), 3);  // weights, activation codes, activation scales
       ptx::mbar_init(ptx::smem_addr(&bars->empty[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&bars->xs_in[s]), 32);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(ptx::smem_addr(&bars->acc_full[a]), 1);
@@ -231,13 +240,16 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
   // After the tensor memory is taken: a CTA of the next grid on this SM can then
   // not take it first and wait for this grid with it in hand.
   ptx::griddep_launch_dependents();
-  const uint32_t tmem_base = bars->tmem_base;
-  const int total = list.tile_begin[p.E];
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+  const int total = __shfl_sync(0xffffffffu, list.tile_begin[p.E], 0);
   if (p.split > 1) {
     // Rank 0's shared memory is only written once it has started.
     ptx::cluster_arrive_relaxed();
     ptx::cluster_wait();
   }
+
+  // Activation scales of one column group in a stage: 512 bytes per 128 rows.
+  const uint32_t group_bytes = ((static_cast<uint32_t>(p.npad) + 127u) >> 7) * 512u;
 
   // Test build only (SPENSE_TEST_HOOKS): to exercise the failure path, the
   // loaders wait (bounded) on a word nothing sets, before any copy is issued.
@@ -259,23 +271,22 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
   if (warp == 5 || warp == 6) {
     // ------------------------------------------------------------ weights
     test_gate_wait();
-    if (lane == 0 && !*abort_flag) {
-      const uint64_t pol = p.w_keep ? ptx::policy_evict_normal() : ptx::policy_evict_first();
-      TileWalker walk(p, list);
-      Ring ring(static_cast<uint32_t>(p.stages));
-      int i = 0;
-      bool ok = true;
-      for (int t = unit; ok && t < total; t += units) {
-        const Tile tile = walk.get(t);
-        const uint8_t* src =
-            p.blocks + (static_cast<size_t>(tile.e) * p.n_tiles + tile.n_tile) * p.kblocks * kMx4BlockBytes;
-        for (int kb = kb0; kb < kb1; ++kb, ++i, ring.advance()) {
-          if ((i & 1) != (warp & 1)) continue;
-          if (!wait_bar(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
-                        abort_flag)) {
-            ok = false;
-            break;
-          }
+    __syncwarp();
+    bool ok = __all_sync(0xffffffffu, !*abort_flag);
+    const uint64_t pol = p.w_keep ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+    TileWalker walk(p, list);
+    Ring ring(static_cast<uint32_t>(p.stages));
+    int i = 0;
+    for (int t = unit; ok && t < total; t += units) {
+      const Tile tile = walk.get(t);
+      const uint8_t* src =
+          p.blocks + (static_cast<size_t>(tile.e) * p.n_tiles + tile.n_tile) * p.kblocks * kMx4BlockBytes;
+      for (int kb = kb0; kb < kb1; ++kb, ++i, ring.advance()) {
+        if ((i & 1) != (warp & 1)) continue;
+        ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
+                      abort_flag);
+        if (!ok) break;
+        if (ptx::elect_one()) {
           const uint32_t full = ptx::smem_addr(&bars->full[ring.s]);
           ptx::mbar_arrive_expect_tx(full, kMx4BlockBytes);
           ptx::bulk_g2s(smem_base + ring.s * p.stage_bytes, src + static_cast<size_t>(kb) * kMx4BlockBytes,
@@ -286,23 +297,22 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
   } else if (warp == 7) {
     // ------------------------------------------------------------ activation codes
     test_gate_wait();
-    if (lane == 0 && !*abort_flag) {
-      ptx::griddep_wait();
-      const uint64_t pol = ptx::policy_evict_last();
-      TileWalker walk(p, list);
-      Ring ring(static_cast<uint32_t>(p.stages));
-      bool ok = true;
-      for (int t = unit; ok && t < total; t += units) {
-        const Tile tile = walk.get(t);
-        const int b = tile.rows <= p.box[0] ? 0 : (tile.rows <= p.box[1] ? 1 : 2);
-        const CUtensorMap* map = b == 0 ? &map0 : (b == 1 ? &map1 : &map2);
-        const uint32_t bytes = static_cast<uint32_t>(p.box[b]) * 128u;
-        for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
-          if (!wait_bar(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
-                        abort_flag)) {
-            ok = false;
-            break;
-          }
+    __syncwarp();
+    bool ok = __all_sync(0xffffffffu, !*abort_flag);
+    ptx::griddep_wait();
+    const uint64_t pol = ptx::policy_evict_last();
+    TileWalker walk(p, list);
+    Ring ring(static_cast<uint32_t>(p.stages));
+    for (int t = unit; ok && t < total; t += units) {
+      const Tile tile = walk.get(t);
+      const int b = tile.rows <= p.box[0] ? 0 : (tile.rows <= p.box[1] ? 1 : 2);
+      const CUtensorMap* map = b == 0 ? &map0 : (b == 1 ? &map1 : &map2);
+      const uint32_t bytes = static_cast<uint32_t>(p.box[b]) * 128u;
+      for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
+        ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
+                      abort_flag);
+        if (!ok) break;
+        if (ptx::elect_one()) {
           const uint32_t full = ptx::smem_addr(&bars->full[ring.s]);
           ptx::mbar_arrive_expect_tx(full, bytes);
           ptx::tma_load_2d(smem_base + ring.s * p.stage_bytes + kMx4BlockBytes, map, kb * 128, tile.row0, full, pol);
@@ -310,98 +320,104 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
       }
     }
   } else if (warp == 8) {
-    // ------------------------------------------------------------ activation scales
+    // ------------------------------------------------------------ activation scales in
     test_gate_wait();
     ptx::griddep_wait();
     TileWalker walk(p, list);
     Ring ring(static_cast<uint32_t>(p.stages));
-    Ring done(static_cast<uint32_t>(p.stages));  // the stage whose copies complete next
-    const uint32_t chunk_bytes = ((static_cast<uint32_t>(p.npad) + 127u) >> 7) * 512u;  // of one column group
-    int pending = 0;
     bool ok = __all_sync(0xffffffffu, !*abort_flag);
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
       for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
-        if (!wait_bar(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
-                      abort_flag))
-          ok = false;
-        ok = __all_sync(0xffffffffu, ok);
+        ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
+                      abort_flag);
         if (!ok) break;
-        const uint32_t dst = smem_base + ring.s * p.stage_bytes + p.xs_off + static_cast<uint32_t>(lane) * 16u;
+        const uint32_t dst = smem_base + ring.s * p.stage_bytes + p.xs_off + static_cast<uint32_t>(lane) * 4u;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int g = 2 * kb + j;
           if (g >= p.groups) break;
           const uint32_t* src = p.xs + static_cast<size_t>(g) * p.T + tile.row0;
           for (int r = lane; r < tile.rows; r += 32)
-            ptx::cp_async4(dst + j * chunk_bytes + static_cast<uint32_t>(r >> 7) * 512u +
-                               static_cast<uint32_t>((r >> 5) & 3) * 4u,
-                           src + r);
+            ptx::cp_async4(dst + j * group_bytes + static_cast<uint32_t>(r - lane) * 4u, src + r);
         }
-        ptx::cp_async_commit();
-        if (++pending == kXsDepth) {
-          ptx::cp_async_wait<kXsDepth - 1>();
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&bars->full[done.s]));
-          done.advance();
-          --pending;
-        }
+        ptx::cp_async_arrive(ptx::smem_addr(&bars->xs_in[ring.s]));
       }
     }
-    ptx::cp_async_wait<0>();
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    for (; pending > 0; --pending, done.advance())
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&bars->full[done.s]));
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ activation scales into tcgen05.cp's order
+    // In place, 128 rows (512 bytes) at a time. A warp of its own: the fence in
+    // front of the tensor core's reads waits for the memory operations the warp
+    // has in flight, so in the loading warp it put one trip to L2 into every block.
+    const int my_tiles = unit < total ? (total - unit + units - 1) / units : 0;
+    const int items = my_tiles * (kb1 - kb0);
+    Ring ring(static_cast<uint32_t>(p.stages));
+    for (int i = 0; i < items; ++i, ring.advance()) {
+      if (!wait_all(ptx::smem_addr(&bars->xs_in[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
+                    abort_flag))
+        break;
+      const uint32_t base = smem_base + ring.s * p.stage_bytes + p.xs_off;
+      for (uint32_t a = 0; a < 2u * group_bytes; a += 512u) {
+        uint32_t w[4];
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) w[q] = ptx::ld_smem_u32(base + a + q * 128u + static_cast<uint32_t>(lane) * 4u);
+        __syncwarp();
+        ptx::st_smem_u4(base + a + static_cast<uint32_t>(lane) * 16u, w[0], w[1], w[2], w[3]);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&bars->full[ring.s]));
+    }
   } else if (warp == 4) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      TileWalker walk(p, list);
-      Ring ring(static_cast<uint32_t>(p.stages));
-      const uint32_t sf_base = tmem_base + static_cast<uint32_t>(p.nacc * p.npad);
-      const uint32_t atoms = (static_cast<uint32_t>(p.npad) + 127u) >> 7;
-      uint32_t sbuf = 0;
-      int u = 0;
-      bool ok = true;
-      for (int t = unit; ok && t < total; t += units, ++u) {
-        const Tile tile = walk.get(t);
-        const uint32_t n = (static_cast<uint32_t>(tile.rows) + 15u) & ~15u;
-        const uint32_t idesc0 = ptx::idesc_mxf4(n, 0), idesc2 = ptx::idesc_mxf4(n, 2);
-        const uint32_t acc = static_cast<uint32_t>(u % p.nacc), aph = static_cast<uint32_t>((u / p.nacc) & 1);
-        if (!wait_bar(ptx::smem_addr(&bars->acc_empty[acc]), aph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_MMA,
-                      abort_flag))
-          break;
+    // The whole warp walks the blocks and one elected lane issues: with control
+    // flow the compiler knows to be uniform, the operands stay in uniform
+    // registers, where these instructions want them.
+    TileWalker walk(p, list);
+    Ring ring(static_cast<uint32_t>(p.stages));
+    const uint32_t sf_base = tmem_base + static_cast<uint32_t>(p.nacc * p.npad);
+    const uint32_t atoms = (static_cast<uint32_t>(p.npad) + 127u) >> 7;
+    uint32_t sbuf = 0, acc = 0, aph = 1;
+    bool ok = true;
+    for (int t = unit; ok && t < total; t += units) {
+      const Tile tile = walk.get(t);
+      const uint32_t idesc = ptx::idesc_mxf4((static_cast<uint32_t>(tile.rows) + 15u) & ~15u, 0);
+      const uint32_t sf2 = ptx::idesc_mxf4(0, 2) ^ ptx::idesc_mxf4(0, 0);
+      ok = wait_all(ptx::smem_addr(&bars->acc_empty[acc]), aph, p.status, SPENSE_DEVICE_TIMEOUT_MMA, abort_flag);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const uint32_t d_tmem = tmem_base + acc * static_cast<uint32_t>(p.npad);
+      for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
+        ok = wait_all(ptx::smem_addr(&bars->full[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_MMA, abort_flag);
+        if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * static_cast<uint32_t>(p.npad);
-        for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
-          if (!wait_bar(ptx::smem_addr(&bars->full[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_MMA,
-                        abort_flag)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
+        if (ptx::elect_one()) {
           const uint32_t a_s = smem_base + ring.s * p.stage_bytes;
-          const uint32_t b_s = a_s + kMx4BlockBytes;
-          const uint32_t xs_s = a_s + p.xs_off;
+          const uint64_t ad = ptx::desc_sw128(a_s), bd = ptx::desc_sw128(a_s + kMx4BlockBytes);
+          const uint64_t wd = ptx::desc_rows16(a_s + kMx4CodeBytes), xd = ptx::desc_rows16(a_s + p.xs_off);
           // Scales: 8 columns for the weights' two column groups, then 8 a group for the activations.
           const uint32_t sfa = sf_base + sbuf * 24u, sfb = sfa + 8u;
+          const uint32_t steps = kb + 1 == p.kblocks ? static_cast<uint32_t>(p.last_steps) : 4u;
 #pragma unroll
           for (uint32_t j = 0; j < 2; ++j) {
-            ptx::tmem_cp_32x128b_x4(sfa + 4u * j, ptx::desc_rows16(a_s + kMx4CodeBytes + 512u * j));
-            for (uint32_t a = 0; a < atoms; ++a)
-              ptx::tmem_cp_32x128b_x4(sfb + 8u * j + 4u * a, ptx::desc_rows16(xs_s + (j * atoms + a) * 512u));
+            ptx::tmem_cp_32x128b_x4(sfa + 4u * j, wd + 32u * j);
+            ptx::tmem_cp_32x128b_x4(sfb + 8u * j, xd + 32u * j * atoms);
+            if (atoms > 1) ptx::tmem_cp_32x128b_x4(sfb + 8u * j + 4u, xd + 32u * j * atoms + 32u);
           }
-          const uint32_t steps = kb + 1 == p.kblocks ? static_cast<uint32_t>(p.last_steps) : 4u;
-          for (uint32_t k = 0; k < steps; ++k)
-            ptx::mma_mxf4(d_tmem, ptx::desc_sw128(a_s + 32u * k), ptx::desc_sw128(b_s + 32u * k),
-                          (k & 1u) ? idesc2 : idesc0, sfa + 4u * (k >> 1), sfb + 8u * (k >> 1),
-                          (kb > kb0 || k > 0) ? 1u : 0u);
-          sbuf ^= 1u;
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            if (k < steps)
+              ptx::mma_mxf4(d_tmem, ad + 2u * k, bd + 2u * k, idesc ^ ((k & 1u) ? sf2 : 0u), sfa + 4u * (k >> 1),
+                            sfb + 8u * (k >> 1), (kb > kb0 || k > 0) ? 1u : 0u);
           ptx::mma_commit(ptx::smem_addr(&bars->empty[ring.s]));
+          if (kb + 1 == kb1) ptx::mma_commit(ptx::smem_addr(&bars->acc_full[acc]));
         }
-        if (!ok) break;
-        ptx::mma_commit(ptx::smem_addr(&bars->acc_full[acc]));
+        __syncwarp();
+        sbuf ^= 1u;
+      }
+      if (++acc == static_cast<uint32_t>(p.nacc)) {
+        acc = 0;
+        aph ^= 1u;
       }
     }
   } else {
@@ -421,34 +437,18 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
       const uint32_t taddr = lane_base + acc * static_cast<uint32_t>(p.npad);
       const int n_warp = tile.n_tile * kMx4Rows + warp * 32;
       uint16_t* const y = p.y + static_cast<int64_t>(tile.row0) * p.ldy;
-      if (rank == 0) {
-        if (p.split > 1) break;  // finished below, once the peers' partials are in
-        for (int c0 = 0; c0 < tile.rows; c0 += 16) {
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c0), v);
-          ptx::tmem_ld_wait();
+      if (p.split > 1) break;  // finished below, with the other CTAs of the cluster
+      for (int c0 = 0; c0 < tile.rows; c0 += 16) {
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c0), v);
+        ptx::tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t q[4];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t q[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              q[j] = bf16x2(__uint_as_float(v[8 * h + 2 * j]), __uint_as_float(v[8 * h + 2 * j + 1]));
-            store_8rows(q, lane, y, p.ldy, c0 + 8 * h, tile.rows, n_warp, p.N);
-          }
-        }
-      } else {
-        // Partial into rank 0: [rank - 1][row / 4][128 weight rows][4 rows].
-        const uint32_t dst = ptx::mapa(recv_base + (rank - 1u) * static_cast<uint32_t>(p.npad) * 512u +
-                                           static_cast<uint32_t>(warp * 32 + lane) * 16u, 0u);
-        for (int c0 = 0; c0 < tile.rows; c0 += 16) {
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c0), v);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            ptx::st_cluster_v4(dst + static_cast<uint32_t>(c0 / 4 + q) * 2048u,
-                               make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                           __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])));
+          for (int j = 0; j < 4; ++j)
+            q[j] = bf16x2(__uint_as_float(v[8 * h + 2 * j]), __uint_as_float(v[8 * h + 2 * j + 1]));
+          store_8rows(q, lane, y, p.ldy, c0 + 8 * h, tile.rows, n_warp, p.N);
         }
       }
       ptx::tc_fence_before();
@@ -457,18 +457,38 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
   }
   __syncwarp();
   if (p.split > 1) {
-    // One tile a cluster at most. Every thread of the cluster meets here: the
-    // peers' partials are in rank 0's shared memory.
+    // One tile a cluster at most. Every thread of the cluster meets here: every
+    // MMA of the cluster has completed, so rank 0's ring is idle and takes the
+    // peers' partials, [rank - 1][row / 4][128 weight rows][4 rows].
+    ptx::tc_fence_before();
     ptx::cluster_arrive();
     ptx::cluster_wait();
-    if (rank == 0 && warp < 4 && unit < total && !*abort_flag) {
-      TileWalker walk(p, list);
-      const Tile tile = walk.get(unit);
-      ptx::tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    ptx::tc_fence_after();
+    const bool work = warp < 4 && unit < total && !*abort_flag;
+    TileWalker walk(p, list);
+    const Tile tile = work ? walk.get(unit) : Tile{0, 0, 0, 0};
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    if (work && rank != 0) {
+      const uint32_t dst = ptx::mapa(smem_base + (rank - 1u) * static_cast<uint32_t>(p.npad) * 512u +
+                                         static_cast<uint32_t>(warp * 32 + lane) * 16u, 0u);
+      for (int c0 = 0; c0 < tile.rows; c0 += 16) {
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c0), v);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          ptx::st_cluster_v4(dst + static_cast<uint32_t>(c0 / 4 + q) * 2048u,
+                             make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                         __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])));
+      }
+    }
+    __syncwarp();
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+    if (work && rank == 0) {
       const int n_warp = tile.n_tile * kMx4Rows + warp * 32;
       uint16_t* const y = p.y + static_cast<int64_t>(tile.row0) * p.ldy;
-      const uint32_t src = recv_base + static_cast<uint32_t>(warp * 32 + lane) * 16u;
+      const uint32_t src = smem_base + static_cast<uint32_t>(warp * 32 + lane) * 16u;
       for (int c0 = 0; c0 < tile.rows; c0 += 16) {
         uint32_t v[16];
         ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c0), v);

@@ -18,6 +18,7 @@ constexpr int kMx4CodeBytes = 16384;
 constexpr int kMx4ScaleBytes = 1024;
 constexpr int kMx4BlockBytes = kMx4CodeBytes + kMx4ScaleBytes;
 
+constexpr int kMx4BarrierBytes = 512;  // mbarriers and flags behind the ring
 constexpr int kMx4MaxExperts = 1024;
 constexpr int64_t kMx4MaxRows = 1 << 20;
 
@@ -36,13 +37,13 @@ struct Mx4GemmParams {
   int box[3];              // rows one activation load covers, smallest first; box[2] == npad
   int stages, nacc;
   int split;               // CTAs of a cluster sharing one tile's K range (1: none)
-  uint32_t stage_bytes, xs_off, recv_bytes, tmem_cols;
+  uint32_t stage_bytes, xs_off, tmem_cols;
   int w_keep;              // 1: weights are read again by later tiles, keep them in L2
 };
 
 struct Mx4GemmPlan {
   int npad, stages, nacc, split, ctas_per_sm, grid;
-  uint32_t stage_bytes, xs_off, recv_bytes, tmem_cols, smem_bytes;
+  uint32_t stage_bytes, xs_off, tmem_cols, smem_bytes;
 };
 
 cudaError_t launch_mx4_gemm(const CUtensorMap (&maps)[3], const Mx4GemmParams& p, int grid, uint32_t smem_bytes,

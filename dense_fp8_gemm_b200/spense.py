@@ -13,6 +13,9 @@ import os
 import numpy as np
 import torch
 
+from torch._C import _cuda_getCurrentRawStream as _raw_stream
+from torch._C import _cuda_getDevice as _device_index
+
 from .build import LIB_PATH, TEST_LIB_PATH
 
 SPENSE_OK = 0
@@ -157,8 +160,12 @@ def _check(code: int, where: str):
 
 
 def _stream(stream) -> ctypes.c_void_p:
+    """The stream's address; None: the current stream of the current device (by
+    its raw address: building torch.cuda.current_stream()'s object takes 3 us)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return ctypes.c_void_p(_raw_stream(_device_index()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -561,9 +568,9 @@ def select_dense(score: torch.Tensor, Kd: int, out: torch.Tensor | None = None, 
 def _current(name: str, *tensors):
     """The device of `tensors`, which has to be the current one: the library
     launches there, and addresses of another device mean nothing on it."""
-    dev = torch.cuda.current_device()
+    dev = _device_index()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
