@@ -1,7 +1,11 @@
 // C entry points of the MXFP4 and expert operators: argument validation, the
 // packed handle and launch planning.
 #include <algorithm>
+#include <array>
 #include <climits>
+#include <cstdlib>
+#include <map>
+#include <mutex>
 #include <new>
 
 #include "abi_util.h"
@@ -18,55 +22,149 @@ struct spense_mx4_packed {
 
 namespace {
 
-constexpr size_t kMx4Workspace = 256;  // the header: status word
+constexpr size_t kMx4Header = 256;  // workspace: status word, then pair mode's scale tiles
 
-// Rows a tile of activations takes, cluster split, ring depth.
+// Shared memory of a CTA that has its SM to itself, or shares it with another.
+constexpr uint32_t kMx4Smem[2] = {232448u, 115200u};
+
+// Clusters of s CTAs, cps to a SM, that the device holds at once.
+int clusters_at_once(int s, int cps, int sms) {
+  static std::mutex mu;
+  static std::map<std::array<int, 3>, int> known;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return sms * cps / (s + 1);
+  std::lock_guard<std::mutex> lk(mu);
+  const auto it = known.find({dev, s, cps});
+  if (it != known.end()) return it->second;
+  int n = 0;
+  if (mx4_max_clusters(s, kMx4Smem[cps - 1], &n) != cudaSuccess) n = sms * cps / (s + 1);
+  known[{dev, s, cps}] = n;
+  return n;
+}
+
+// Estimated time of a launch, in microseconds, from measured rates of this
+// kernel: a CTA takes 0.27 us a block and 0.0006 more a row of the tile (latency
+// of its ring), all CTAs together 12.4 TB/s from L2 and the weights 5.5 TB/s from
+// HBM; two CTAs on a SM take half as long again each; 3.2 us go before and after
+// the blocks, 6 ns a row into the epilogue, 0.8 us and 12 ns a row into the exchange
+// of a split tile's partials. Against a sweep of 5 shapes x 7 row counts (M 1 ..
+// 1024) x tiles x splits the choices by it are within 20 % of the best.
+double mx4_cost(int n, int split, int cps, int64_t tiles, int kblocks, double weight_bytes, int sms) {
+  const int64_t ctas = tiles * split;
+  const double blocks = split == 1 ? static_cast<double>((tiles + sms - 1) / sms) * kblocks : (kblocks + split - 1) / split;
+  const double l2 = (kMx4BlockBytes + n * 136.0) * static_cast<double>(std::min<int64_t>(ctas, sms)) / 12.4e6;
+  const double block = std::max(0.27 + 0.0006 * n, l2) * (cps == 2 ? 1.5 : 1.0);
+  const double t = 3.2 + 0.006 * n + blocks * block + (split > 1 ? 0.8 + 0.012 * n : 0.0);
+  return std::max(t, 3.2 + weight_bytes / 5.5e6) + 0.05 * t;
+}
+
+// Rows a tile of activations takes, CTA pairs, cluster split, ring depth.
 //
-// A tile reads its weight block and its activation rows for every 256 columns
-// of K; up to 256 rows one tile takes all of them, so that weights are read
-// once. With experts the device alone knows who has how many rows: room for
+// A tile reads its weight block and its activation rows for every 256 columns of
+// K. Dense products: rows in equal tiles of at most 240, as many as mx4_cost
+// likes. With experts the device alone knows who has how many rows: room for
 // twice the average, since a heavier expert only costs a second reading of its
 // weights (from L2) and smaller tiles leave a deeper ring.
 //
-// Few tiles: the largest cluster (8 CTAs at most) that two CTAs a SM can hold at
-// once, that leaves each CTA two blocks or more, and whose partials fit the ring.
-spense_status make_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, Mx4GemmPlan* out) {
+// Few tiles: clusters of up to 8 CTAs split K, when the device holds all of them
+// at once and their partials fit the ring.
+//
+// Pairs (256 weight rows and up to 224 activation rows by two SMs) read a third
+// fewer bytes from L2 for the same products; they pay from 3e11 flops on, where
+// that outweighs the launch that orders their scales: 51200x5120 at 512, 1024 and
+// 8192 rows 74 -> 72, 128 -> 114 and 965 -> 845 us, but 10240x5120 at 2048 rows
+// 53 -> 56 us. Experts also need 128 rows on average, or a pair's tile is mostly
+// weights.
+spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, Mx4GemmPlan* out) {
   Mx4GemmPlan pl{};
-  const int64_t want = ragged ? std::max<int64_t>(2 * ((T + E - 1) / E), 32) : T;
-  pl.npad = static_cast<int>(std::min<int64_t>(256, round_up(static_cast<size_t>(std::min(want, T)), 16)));
-  const int64_t row_tiles = ragged ? std::min(E, T) + T / pl.npad : (T + pl.npad - 1) / pl.npad;
-  const int64_t tiles = row_tiles * n_tiles;
-  if (tiles > INT_MAX / 2) return fail(SPENSE_ERR_SHAPE, "too many tiles for one launch (%lld)", (long long)tiles);
-  const uint32_t atoms = (static_cast<uint32_t>(pl.npad) + 127u) / 128u;
-  pl.xs_off = kMx4BlockBytes + static_cast<uint32_t>(pl.npad) * 128u;
-  pl.stage_bytes = pl.xs_off + atoms * 1024u;
   const uint32_t tail = static_cast<uint32_t>(round_up(kMx4BarrierBytes + 4 * (3 * static_cast<size_t>(E) + 1), 16));
-  // Ring stages with `cps` CTAs a SM.
-  auto ring = [&](int cps) {
-    const uint32_t budget = cps == 2 ? 115200u : 232448u, fixed = 1024 + tail;
-    return static_cast<int>(std::min<uint32_t>(12, (budget - fixed) / pl.stage_bytes));
+  const int64_t active = ragged ? std::min(E, T) : 1;
+  const double flops = 2.0 * T * n_tiles * kMx4Rows * kblocks * kMx4Cols;
+  const int64_t avg = (T + E - 1) / E;
+  pl.pair = flops >= 3e11 && (ragged ? avg : T) >= 128 ? 1 : 0;
+  const int most = pl.pair ? 224 : kMx4MaxTile, step = pl.pair ? 32 : 16;
+  // Row tiles at most: every expert's last one may be short.
+  auto row_tiles = [&](int n) { return ragged ? active + T / n : (T + n - 1) / n; };
+  auto stage = [&](int n) {
+    return kMx4BlockBytes + static_cast<uint32_t>(pl.pair ? n / 2 : n) * 128u + (pl.pair ? kMx4XsTileBytes : 0u);
   };
-  pl.split = 1;
-  pl.ctas_per_sm = 1;
-  if (pl.npad <= 64 && tiles < sms)
-    for (int s = 8; s > 1 && pl.split == 1; --s) {
-      const int cps = tiles * s > sms ? 2 : 1;
-      if (tiles * s <= 2 * sms && kblocks >= 2 * s && ring(cps) >= 3 &&
-          static_cast<uint32_t>((s - 1) * pl.npad * 512) <= static_cast<uint32_t>(ring(cps)) * pl.stage_bytes) {
+  auto slot = [&](int n) { return pl.pair ? 0u : (n > 61 ? 2048u : 1024u); };
+  auto ring = [&](int n, int cps) {
+    const uint32_t fixed = 1024 + tail + kMx4XsSlots * slot(n);
+    return static_cast<int>(std::min<uint32_t>(12, (kMx4Smem[cps - 1] - fixed) / stage(n)));
+  };
+  pl.split = pl.ctas_per_sm = 1;
+  const double weight_bytes = static_cast<double>(active) * n_tiles * kblocks * kMx4BlockBytes;
+  const int64_t m0 = ragged ? 1 : (T + most - 1) / most;
+  double best = 0.0;
+  for (int64_t m = m0; m < m0 + (ragged || pl.pair ? 1 : 16); ++m) {
+    int n;
+    if (ragged)
+      n = avg >= 112 ? 224 : static_cast<int>(std::min<int64_t>(round_up(std::max<int64_t>(2 * avg, 32), 16), 224));
+    else
+      n = static_cast<int>(round_up((T + m - 1) / m, step));
+    n = static_cast<int>(std::min<int64_t>(n, round_up(T, step)));
+    const int64_t tiles = row_tiles(n) * n_tiles;
+    for (int s = 1; s <= (pl.pair ? 1 : 8); ++s) {
+      const int cps = s > 1 && tiles * s > sms ? 2 : 1;
+      if (s > 1) {
+        if (tiles * s > 2 * sms || kblocks < 2 * s || ring(n, cps) < 3 || n + 48 > 512 / cps) break;
+        const size_t partials = static_cast<size_t>(s - 1) * round_up((n + s - 1) / s, 8) * 512;
+        if (partials > static_cast<size_t>(ring(n, cps)) * stage(n) || tiles > clusters_at_once(s, cps, sms)) continue;
+      }
+      const double c = mx4_cost(n, s, cps, tiles, kblocks, weight_bytes, sms);
+      if (best == 0.0 || c < best) {
+        best = c;
+        pl.npad = n;
         pl.split = s;
         pl.ctas_per_sm = cps;
       }
     }
-  pl.grid = static_cast<int>(pl.split > 1 ? tiles * pl.split : std::min<int64_t>(tiles, sms));
+    if (n <= step) break;
+  }
+  pl.row_tiles = row_tiles(pl.npad);
+  const int64_t tiles = pl.row_tiles * (pl.pair ? (n_tiles + 1) / 2 : n_tiles);
+  if (tiles > INT_MAX / 8) return fail(SPENSE_ERR_SHAPE, "too many tiles for one launch (%lld)", (long long)tiles);
+  pl.grid = static_cast<int>(pl.pair        ? 2 * std::min<int64_t>(tiles, sms / 2)
+                             : pl.split > 1 ? tiles * pl.split
+                                            : std::min<int64_t>(tiles, sms));
+  pl.stage_bytes = stage(pl.npad);
+  pl.xs_bytes = slot(pl.npad);
+  pl.stages = ring(pl.npad, pl.ctas_per_sm);
+  if (pl.stages < 3) return fail(SPENSE_ERR_SHAPE, "no launch plan for %lld experts", (long long)E);
   pl.nacc = pl.split == 1 && 2 * pl.npad + 48 <= 512 ? 2 : 1;
   pl.tmem_cols = 32;
   while (pl.tmem_cols < static_cast<uint32_t>(pl.nacc * pl.npad + 48)) pl.tmem_cols <<= 1;
-  pl.stages = ring(pl.ctas_per_sm);
-  if (pl.stages < 3) return fail(SPENSE_ERR_SHAPE, "no launch plan for %lld experts", (long long)E);
-  pl.smem_bytes = 1024 + tail + static_cast<uint32_t>(pl.stages) * pl.stage_bytes;
+  pl.smem_bytes = 1024 + tail + kMx4XsSlots * pl.xs_bytes + static_cast<uint32_t>(pl.stages) * pl.stage_bytes;
   // A CTA that takes more than half of the tensor memory has the SM to itself.
   if (pl.tmem_cols > 256) pl.smem_bytes = std::max<uint32_t>(pl.smem_bytes, 122880u);
+  pl.workspace_bytes = kMx4Header + (pl.pair ? static_cast<size_t>(pl.row_tiles) * kblocks * kMx4XsTileBytes : 0);
   *out = pl;
+  return SPENSE_OK;
+}
+
+// The search takes some 3 us; a thread keeps the plans of its last shapes.
+spense_status make_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, Mx4GemmPlan* out) {
+  struct Known {
+    std::array<int64_t, 6> key{};
+    Mx4GemmPlan plan{};
+  };
+  static thread_local std::array<Known, 64> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+  const std::array<int64_t, 6> key = {E, n_tiles, kblocks, T, (ragged ? 1 : 2) + 4 * (dev + 1), sms};
+  uint64_t h = 0;
+  for (const int64_t k : key) h = (h ^ static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull;
+  Known& slot = known[h >> 58];
+  if (slot.key != key) {
+    const spense_status st = search_mx4_plan(E, n_tiles, kblocks, T, ragged, sms, &slot.plan);
+    if (st != SPENSE_OK) {
+      slot.key = {};
+      return st;
+    }
+    slot.key = key;
+  }
+  *out = slot.plan;
   return SPENSE_OK;
 }
 
@@ -91,8 +189,6 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
     return fail(SPENSE_ERR_ALIGN, "Xq, x_scale and Y must be 16-byte aligned");
   if (workspace == nullptr) return fail(SPENSE_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned(workspace, 256)) return fail(SPENSE_ERR_ALIGN, "workspace is not 256-byte aligned");
-  if (workspace_bytes < kMx4Workspace)
-    return fail(SPENSE_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", workspace_bytes, kMx4Workspace);
   int dev = 0;
   DeviceInfo info;
   spense_status st = current_device(&dev, &info);
@@ -103,22 +199,49 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
   Mx4GemmPlan pl;
   st = make_mx4_plan(h->E, h->n_tiles, h->kblocks, T, offsets != nullptr, info.sms, &pl);
   if (st != SPENSE_OK) return st;
+  if (workspace_bytes < pl.workspace_bytes)
+    return fail(SPENSE_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", workspace_bytes, pl.workspace_bytes);
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return fail(SPENSE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   Mx4GemmParams p{};
-  CUtensorMap maps[3];
+  Mx4GemmMaps maps;
   for (int i = 0; i < 3; ++i) {
-    p.box[i] = std::min(pl.npad, i == 0 ? 16 : (i == 1 ? 64 : 256));
+    p.box[i] = std::min(pl.pair ? pl.npad / 2 : pl.npad, i == 0 ? 16 : (i == 1 ? 64 : 256));
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(h->K / 2), static_cast<cuuint64_t>(T)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(h->K / 2)};
     const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(p.box[i])};
     const cuuint32_t estr[2] = {1u, 1u};
-    const CUresult r = encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(Xq), dims, strides, box,
+    const CUresult r = encode(&maps.x[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(Xq), dims, strides, box,
                               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(SPENSE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
+  const int64_t groups = (h->K + 127) / 128;
+  if (groups * T > INT_MAX)
+    return fail(SPENSE_ERR_SHAPE, "too many activation scales for one launch (%lld words)", (long long)(groups * T));
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t dims[1] = {static_cast<cuuint64_t>(groups * T)};
+    const cuuint64_t strides[1] = {0};  // a one-dimensional map has none
+    const cuuint32_t box[1] = {i == 0 ? 64u : 256u}, estr[1] = {1u};
+    const CUresult r = encode(i == 0 ? &maps.xs_narrow : &maps.xs_wide, CU_TENSOR_MAP_DATA_TYPE_UINT32, 1,
+                              const_cast<uint8_t*>(x_scale), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(SPENSE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  for (int i = 0; pl.pair && i < 2; ++i) {
+    const uint32_t rows = (i == 0 ? kMx4BlockBytes : kMx4XsTileBytes) / 128;
+    const cuuint64_t blocks = (i == 0 ? static_cast<cuuint64_t>(h->E) * h->n_tiles : pl.row_tiles) * h->kblocks;
+    const cuuint64_t dims[2] = {32, blocks * rows};
+    const cuuint64_t strides[1] = {128};
+    const cuuint32_t box[2] = {32u, rows}, estr[2] = {1u, 1u};
+    const CUresult r = encode(i == 0 ? &maps.w : &maps.xs_tiles, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2,
+                              i == 0 ? h->blocks : ws + kMx4Header, dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(SPENSE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
   p.blocks = h->blocks;
   p.xs = reinterpret_cast<const uint32_t*>(x_scale);
   p.y = Y;
@@ -137,18 +260,23 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
   p.T = static_cast<int>(T);
   p.n_tiles = h->n_tiles;
   p.kblocks = h->kblocks;
-  p.groups = static_cast<int>((h->K + 127) / 128);
+  p.groups = static_cast<int>(groups);
   const int tail_cols = static_cast<int>(h->K - static_cast<int64_t>(h->kblocks - 1) * kMx4Cols);
   p.last_steps = (tail_cols + 63) / 64;
   p.npad = pl.npad;
   p.stages = pl.stages;
   p.nacc = pl.nacc;
   p.split = pl.split;
+  p.pair = pl.pair;
   p.stage_bytes = pl.stage_bytes;
-  p.xs_off = pl.xs_off;
+  p.xs_bytes = pl.xs_bytes;
   p.tmem_cols = pl.tmem_cols;
   p.w_keep = T > pl.npad ? 1 : 0;
-  const cudaError_t e = launch_mx4_gemm(maps, p, pl.grid, pl.smem_bytes, static_cast<cudaStream_t>(stream));
+  cudaError_t e = cudaSuccess;
+  if (pl.pair)
+    e = launch_mx4_scale_tiles(p, static_cast<int>(pl.row_tiles), reinterpret_cast<uint32_t*>(ws + kMx4Header),
+                               static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = launch_mx4_gemm(maps, p, pl.grid, pl.smem_bytes, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "mx4 gemm launch");
   return ok();
 }
@@ -219,7 +347,7 @@ spense_status spense_mx4_pack(const uint8_t* Wq, const uint8_t* w_scale, int64_t
   spense_status st = check_mx4_types(0, K);
   if (st != SPENSE_OK) return st;
   const int64_t n_tiles = (N + kMx4Rows - 1) / kMx4Rows, kblocks = (K + kMx4Cols - 1) / kMx4Cols;
-  if (E * n_tiles * kblocks > INT_MAX)
+  if (E * n_tiles * kblocks > INT_MAX / (kMx4BlockBytes / 128))
     return fail(SPENSE_ERR_SHAPE, "too many blocks for one weight (%lld)", (long long)(E * n_tiles * kblocks));
   if (!aligned(Wq, 16)) return fail(SPENSE_ERR_ALIGN, "Wq is not 16-byte aligned");
   int dev = 0;
@@ -280,7 +408,18 @@ size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M) {
     fail(SPENSE_ERR_ARG, "Wp is NULL or M outside [0, 2^20]");
     return 0;
   }
-  return kMx4Workspace;
+  if (M == 0) return kMx4Header;
+  int dev = 0;
+  DeviceInfo info;
+  if (current_device(&dev, &info) != SPENSE_OK) return 0;
+  // A weight of one expert serves both products, which may be planned differently.
+  size_t bytes = 0;
+  for (int ragged = Wp->E > 1 ? 1 : 0; ragged < 2; ++ragged) {
+    Mx4GemmPlan pl;
+    if (make_mx4_plan(Wp->E, Wp->n_tiles, Wp->kblocks, M, ragged != 0, info.sms, &pl) != SPENSE_OK) return 0;
+    bytes = std::max(bytes, pl.workspace_bytes);
+  }
+  return bytes;
 }
 
 spense_status spense_mx4_gemm(const spense_mx4_packed* Wp, const uint8_t* Xq, const uint8_t* x_scale, int64_t M,

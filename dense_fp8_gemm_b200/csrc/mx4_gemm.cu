@@ -21,13 +21,13 @@
 //   warp 7    TMA loads of the activation codes, in the smallest of three box
 //             heights that covers the tile's rows;
 //   warps 8,9 the activation scales: one word (128 columns) a row. Warp 8 brings
-//             them in with 4-byte asynchronous copies (coalesced, since the words
-//             of neighbouring rows are neighbours in memory), warp 9 puts them
-//             into the order tcgen05.cp reads (lane l, word w: row 32 w + l).
+//             them in by TMA as they lie in memory, warp 9 puts them into the
+//             order tcgen05.cp reads (lane l, word w: row 32 w + l). They have a
+//             ring of their own, so that this step is done ahead of the codes.
 //
-// Few tiles (p.split > 1): the CTAs of a cluster split a tile's K range; the
-// peers store their fp32 partials into rank 0's shared memory and rank 0 adds
-// them in rank order, so the result does not depend on timing.
+// Few tiles (p.split > 1): the CTAs of a cluster split a tile's K range, exchange
+// their fp32 partials through shared memory and finish a share of the tile's rows
+// each, adding the partials in rank order: the result does not depend on timing.
 //
 // Every wait is bounded (1.5 s); on expiry the kernel records a code in the
 // workspace's status word and all roles leave their loops.
@@ -36,6 +36,7 @@
 
 #include "mx4_internal.h"
 #include "mx4_ptx.cuh"
+#include "pdl.cuh"
 #include "spense.h"
 
 namespace spense {
@@ -44,11 +45,14 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 1500000000ull;
 constexpr int kMaxMx4Stages = 12;
 constexpr int kMx4Threads = 320;
+constexpr int kXsSlots = kMx4XsSlots;
 
 struct alignas(16) Mx4Barriers {
   uint64_t full[kMaxMx4Stages];
   uint64_t empty[kMaxMx4Stages];
-  uint64_t xs_in[kMaxMx4Stages];  // a stage's activation scales have landed, in row order
+  uint64_t xs_in[kXsSlots];     // a slot's activation scales have landed, in row order
+  uint64_t xs_full[kXsSlots];   // ... are in the tensor core's order
+  uint64_t xs_empty[kXsSlots];  // ... are in tensor memory
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint32_t tmem_base;
@@ -56,13 +60,16 @@ struct alignas(16) Mx4Barriers {
 };
 static_assert(sizeof(Mx4Barriers) <= kMx4BarrierBytes, "barrier area too small");
 
+// kCluster: the barrier is signalled from another CTA too (acquire at cluster scope).
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned int* status, unsigned int code,
                                          volatile int* abort_flag) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+  auto done = [&] { return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const uint64_t t0 = ptx::globaltimer();
   uint32_t it = 0;
   while (true) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (done()) return true;
     if ((++it & 63u) == 0) {
       if (*abort_flag) return false;
       if (ptx::globaltimer() - t0 > kWaitLimitNs) {
@@ -75,15 +82,45 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned
 }
 
 // The same by a whole (converged) warp, which takes one decision.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, unsigned int* status, unsigned int code,
                                          volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, code, abort_flag));
+  return __all_sync(0xffffffffu, wait_bar<kCluster>(bar, parity, status, code, abort_flag));
+}
+
+// Rows [lo, hi) of expert e, for the 32 experts from e0 at once (lane l: e0 + l).
+// Offsets are cut to [0, T] and to their running maximum (`carry`, over the calls),
+// so ranges never overlap and no offset leads outside the buffers.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int E, int T, int e0, int lane, int& carry, int& lo,
+                                            int& hi) {
+  const int e = e0 + lane;
+  lo = 0;
+  hi = e < E ? T : 0;
+  if (offsets == nullptr) return;
+  int most = e < E ? min(max(__ldg(offsets + e), 0), T) : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, most, o);
+    if (lane >= o) most = max(most, v);
+  }
+  lo = max(most, carry);
+  carry = __shfl_sync(0xffffffffu, lo, 31);
+  hi = e < E ? max(min(__ldg(offsets + e + 1), T), lo) : lo;
+}
+
+// Inclusive sum over the warp.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
 }
 
 // The tile list. tile_begin[e] .. tile_begin[e + 1]: expert e's tiles, its row
 // tiles of npad activation rows consecutive for each weight tile. first[e],
-// count[e]: its rows. Offsets are cut to [0, T] and to ascending order, so no
-// value of theirs leads outside the buffers.
+// count[e]: its rows.
 struct TileList {
   int* tile_begin;
   int* first;
@@ -92,8 +129,21 @@ struct TileList {
 
 struct Tile {
   int e, n_tile, row0, rows;
+  int row_tile;  // number of the row tile among all experts'
 };
 
+template <bool kPair>
+__device__ __forceinline__ int weight_tiles(const Mx4GemmParams& p) {
+  return kPair ? (p.n_tiles + 1) / 2 : p.n_tiles;
+}
+
+// The MMA's N for a tile of so many rows: a multiple of 16, for a pair of 32.
+template <bool kPair>
+__device__ __forceinline__ int mma_rows(int rows) {
+  return kPair ? (rows + 31) & ~31 : (rows + 15) & ~15;
+}
+
+template <bool kPair>
 struct TileWalker {
   const Mx4GemmParams& p;
   const TileList& list;
@@ -109,7 +159,8 @@ struct TileWalker {
     const int nt = local / m_tiles;
     const int r = (local - nt * m_tiles) * p.npad;
     return Tile{__shfl_sync(0xffffffffu, e, 0), __shfl_sync(0xffffffffu, nt, 0),
-                __shfl_sync(0xffffffffu, list.first[e] + r, 0), __shfl_sync(0xffffffffu, min(p.npad, cnt - r), 0)};
+                __shfl_sync(0xffffffffu, list.first[e] + r, 0), __shfl_sync(0xffffffffu, min(p.npad, cnt - r), 0),
+                __shfl_sync(0xffffffffu, list.tile_begin[e] / weight_tiles<kPair>(p) + r / p.npad, 0)};
   }
 };
 
@@ -129,51 +180,68 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Stores a warp's 32 weight rows x 8 activation rows. Lane l holds rows c ..
-// c + 7 of its weight row as four bf16 pairs; three exchange rounds (with lanes
-// 1, 2 and 4 apart) leave it with eight consecutive weight rows (8 (l / 8) ..) of
-// activation row c + l % 8: one 16-byte store, 64 contiguous bytes a row. No
-// shared memory, and a quarter of the instructions of one store a value.
-__device__ __forceinline__ void store_8rows(const uint32_t (&p)[4], int lane, uint16_t* y, int64_t ldy, int c, int rows,
-                                            int n_warp, int N) {
+// Stores a warp's 32 weight rows x (8 kGroups) activation rows. Lane l holds the
+// fp32 sums of its weight row, n_warp + l, for activation rows c .. c + 8 kGroups -
+// 1. As bf16 pairs they go through three exchange rounds (with lanes 1, 2 and 4
+// apart) that leave each lane with eight consecutive weight rows (8 (l / 8) ..) of
+// activation row c + l % 8 of every eight: one 16-byte store a group, 64
+// contiguous bytes a row, without shared memory. The rounds of all groups are
+// interleaved to cover the exchanges' latency.
+template <int kGroups>
+__device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y, int64_t ldy, int c, int rows,
+                                           int n_warp, int N) {
   const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
-  uint32_t q[4];
+  uint32_t q[kGroups][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t o = __shfl_xor_sync(0xffffffffu, p[j], 1);
-    q[j] = b0 ? __byte_perm(o, p[j], 0x7632) : __byte_perm(p[j], o, 0x5410);
-  }
-  uint32_t r[2][2];
+  for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t o = __shfl_xor_sync(0xffffffffu, b1 ? q[2 * i] : q[2 * i + 1], 2);
-    r[i][0] = b1 ? o : q[2 * i];
-    r[i][1] = b1 ? q[2 * i + 1] : o;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t v = bf16x2(a[8 * g + 2 * j], a[8 * g + 2 * j + 1]);
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 1);
+      q[g][j] = b0 ? __byte_perm(o, v, 0x7632) : __byte_perm(v, o, 0x5410);
+    }
+  uint32_t r[kGroups][4];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, b1 ? q[g][2 * i] : q[g][2 * i + 1], 2);
+      r[g][2 * i] = b1 ? o : q[g][2 * i];
+      r[g][2 * i + 1] = b1 ? q[g][2 * i + 1] : o;
+    }
+  uint4 v[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const uint32_t o0 = __shfl_xor_sync(0xffffffffu, b2 ? r[g][0] : r[g][2], 4);
+    const uint32_t o1 = __shfl_xor_sync(0xffffffffu, b2 ? r[g][1] : r[g][3], 4);
+    v[g] = b2 ? make_uint4(o0, o1, r[g][2], r[g][3]) : make_uint4(r[g][0], r[g][1], o0, o1);
   }
-  const uint32_t o0 = __shfl_xor_sync(0xffffffffu, b2 ? r[0][0] : r[1][0], 4);
-  const uint32_t o1 = __shfl_xor_sync(0xffffffffu, b2 ? r[0][1] : r[1][1], 4);
-  const uint4 v = b2 ? make_uint4(o0, o1, r[1][0], r[1][1]) : make_uint4(r[0][0], r[0][1], o0, o1);
-  const int m = c + (lane & 7);
-  const int n = n_warp + (lane >> 3) * 8;
-  if (m >= rows || n >= N) return;
+  const int m = c + (lane & 7), n = n_warp + (lane >> 3) * 8;
   uint16_t* dst = y + m * ldy + n;
-  if (n + 8 <= N && (ldy & 7) == 0) {
-    ptx::st_global_v4(dst, v);
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (n_warp + 32 <= N && (ldy & 7) == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (n + i < N) dst[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    for (int g = 0; g < kGroups; ++g, dst += 8 * ldy)
+      if (m + 8 * g < rows) ptx::st_global_v4(dst, v[g]);
+  } else {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g, dst += 8 * ldy) {
+      const uint32_t w[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
+      if (m + 8 * g < rows)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (n + i < N) dst[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
   }
 }
 
-__global__ void __launch_bounds__(kMx4Threads, 2)
-    spense_mx4_gemm_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
-                           const __grid_constant__ CUtensorMap map2, const __grid_constant__ Mx4GemmParams p) {
+template <bool kPair>
+__global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
+    spense_mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const __grid_constant__ Mx4GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;  // the swizzled tiles are 1024-byte aligned
-  uint8_t* const tail = smem_raw + (smem_base - raw) + static_cast<uint32_t>(p.stages) * p.stage_bytes;
+  const uint32_t xs_base = smem_base + static_cast<uint32_t>(p.stages) * p.stage_bytes;  // the scales' own ring
+  uint8_t* const tail = smem_raw + (xs_base - raw) + (kPair ? 0u : kXsSlots * p.xs_bytes);
   Mx4Barriers* const bars = reinterpret_cast<Mx4Barriers*>(tail);
   TileList list;
   list.tile_begin = reinterpret_cast<int*>(tail + kMx4BarrierBytes);
@@ -183,53 +251,55 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = p.split > 1 ? ptx::cluster_ctarank() : 0u;
-  const int unit = static_cast<int>(blockIdx.x) / p.split;  // tiles unit, unit + units, ..
-  const int units = static_cast<int>(gridDim.x) / p.split;
-  const int kb0 = static_cast<int>(static_cast<long long>(p.kblocks) * rank / p.split);
-  const int kb1 = static_cast<int>(static_cast<long long>(p.kblocks) * (rank + 1) / p.split);
+  const bool split = !kPair && p.split > 1;
+  const uint32_t rank = kPair || split ? ptx::cluster_ctarank() : 0u;
+  const int per_unit = kPair ? 2 : p.split;
+  const int unit = static_cast<int>(blockIdx.x) / per_unit;  // tiles unit, unit + units, ..
+  const int units = static_cast<int>(gridDim.x) / per_unit;
+  const int kb0 = kPair ? 0 : static_cast<int>(static_cast<long long>(p.kblocks) * rank / p.split);
+  const int kb1 = kPair ? p.kblocks : static_cast<int>(static_cast<long long>(p.kblocks) * (rank + 1) / p.split);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      ptx::mbar_init(ptx::smem_addr(&bars->full[s]), 3);  // weights, activation codes, activation scales
+      ptx::mbar_init(ptx::smem_addr(&bars->full[s]), 2);  // weights, activation codes
       ptx::mbar_init(ptx::smem_addr(&bars->empty[s]), 1);
-      ptx::mbar_init(ptx::smem_addr(&bars->xs_in[s]), 32);
+    }
+    for (int s = 0; s < kXsSlots; ++s) {
+      ptx::mbar_init(ptx::smem_addr(&bars->xs_in[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&bars->xs_full[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&bars->xs_empty[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(ptx::smem_addr(&bars->acc_full[a]), 1);
-      ptx::mbar_init(ptx::smem_addr(&bars->acc_empty[a]), 128);
+      // pair mode: the odd CTA's epilogue arrives once, remotely
+      ptx::mbar_init(ptx::smem_addr(&bars->acc_empty[a]), kPair ? 129 : 128);
     }
     bars->abort_flag = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 4) {
-    ptx::tmem_alloc(ptx::smem_addr(&bars->tmem_base), p.tmem_cols);
-    ptx::tmem_relinquish();
+    if constexpr (kPair) {
+      ptx::tmem_alloc_pair(ptx::smem_addr(&bars->tmem_base), p.tmem_cols);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(ptx::smem_addr(&bars->tmem_base), p.tmem_cols);
+      ptx::tmem_relinquish();
+    }
   }
   if (p.offsets != nullptr) ptx::griddep_wait();  // the offsets may be the previous grid's
   if (warp == 0) {
-    int begin = 0;
+    int begin = 0, carry = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      int lo = 0, hi = 0;
+      int lo, hi;
+      expert_rows(p.offsets, p.E, p.T, e0, lane, carry, lo, hi);
+      const int tiles = (hi - lo + p.npad - 1) / p.npad * weight_tiles<kPair>(p);
+      const int scan = warp_scan(tiles, lane);
       if (e < p.E) {
-        lo = 0;
-        hi = p.T;
-        if (p.offsets != nullptr) {
-          lo = min(max(__ldg(p.offsets + e), 0), p.T);
-          hi = min(max(__ldg(p.offsets + e + 1), lo), p.T);
-        }
         list.first[e] = lo;
         list.count[e] = hi - lo;
+        list.tile_begin[e] = begin + scan - tiles;
       }
-      const int tiles = (hi - lo + p.npad - 1) / p.npad * p.n_tiles;
-      int scan = tiles;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += v;
-      }
-      if (e < p.E) list.tile_begin[e] = begin + scan - tiles;
       begin += __shfl_sync(0xffffffffu, scan, 31);
     }
     if (lane == 0) list.tile_begin[p.E] = begin;
@@ -242,14 +312,15 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
   ptx::griddep_launch_dependents();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   const int total = __shfl_sync(0xffffffffu, list.tile_begin[p.E], 0);
-  if (p.split > 1) {
-    // Rank 0's shared memory is only written once it has started.
+  if (kPair || split) {
+    // The other CTAs' barriers and shared memory are only touched once they have started.
     ptx::cluster_arrive_relaxed();
     ptx::cluster_wait();
   }
 
-  // Activation scales of one column group in a stage: 512 bytes per 128 rows.
-  const uint32_t group_bytes = ((static_cast<uint32_t>(p.npad) + 127u) >> 7) * 512u;
+  // Activation scales of one column group in a stage: up to 61 rows one narrow
+  // box and one tcgen05.cp, else a wide box and one or two.
+  const uint32_t group_bytes = kPair || p.npad > 61 ? 1024u : 512u;
 
   // Test build only (SPENSE_TEST_HOOKS): to exercise the failure path, the
   // loaders wait (bounded) on a word nothing sets, before any copy is issued.
@@ -274,23 +345,31 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
     __syncwarp();
     bool ok = __all_sync(0xffffffffu, !*abort_flag);
     const uint64_t pol = p.w_keep ? ptx::policy_evict_normal() : ptx::policy_evict_first();
-    TileWalker walk(p, list);
+    TileWalker<kPair> walk(p, list);
     Ring ring(static_cast<uint32_t>(p.stages));
     int i = 0;
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
-      const uint8_t* src =
-          p.blocks + (static_cast<size_t>(tile.e) * p.n_tiles + tile.n_tile) * p.kblocks * kMx4BlockBytes;
+      // Pair mode: the pair's two weight tiles, one a CTA (past the last tile the
+      // last one again; those results are not stored).
+      const int wt = kPair ? min(2 * tile.n_tile + static_cast<int>(rank), p.n_tiles - 1) : tile.n_tile;
+      const int wt0 = (tile.e * p.n_tiles + wt) * p.kblocks;  // the weight tile's first block
+      const uint8_t* src = p.blocks + static_cast<size_t>(wt0) * kMx4BlockBytes;
       for (int kb = kb0; kb < kb1; ++kb, ++i, ring.advance()) {
         if ((i & 1) != (warp & 1)) continue;
         ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
                       abort_flag);
         if (!ok) break;
         if (ptx::elect_one()) {
-          const uint32_t full = ptx::smem_addr(&bars->full[ring.s]);
-          ptx::mbar_arrive_expect_tx(full, kMx4BlockBytes);
-          ptx::bulk_g2s(smem_base + ring.s * p.stage_bytes, src + static_cast<size_t>(kb) * kMx4BlockBytes,
-                        kMx4BlockBytes, full, pol);
+          const uint32_t full = ptx::smem_addr(&bars->full[ring.s]), dst = smem_base + ring.s * p.stage_bytes;
+          if constexpr (kPair) {
+            // Both CTAs' copies are counted on the even CTA's barrier.
+            if (rank == 0) ptx::mbar_arrive_expect_tx(full, 2 * kMx4BlockBytes);
+            ptx::tma_load_2d_pair(dst, &maps.w, 0, (wt0 + kb) * (kMx4BlockBytes / 128), ptx::mapa(full, 0u), pol);
+          } else {
+            ptx::mbar_arrive_expect_tx(full, kMx4BlockBytes);
+            ptx::bulk_g2s(dst, src + static_cast<size_t>(kb) * kMx4BlockBytes, kMx4BlockBytes, full, pol);
+          }
         }
       }
     }
@@ -301,12 +380,15 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
     bool ok = __all_sync(0xffffffffu, !*abort_flag);
     ptx::griddep_wait();
     const uint64_t pol = ptx::policy_evict_last();
-    TileWalker walk(p, list);
+    TileWalker<kPair> walk(p, list);
     Ring ring(static_cast<uint32_t>(p.stages));
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
-      const int b = tile.rows <= p.box[0] ? 0 : (tile.rows <= p.box[1] ? 1 : 2);
-      const CUtensorMap* map = b == 0 ? &map0 : (b == 1 ? &map1 : &map2);
+      // Pair mode: each CTA holds half of the MMA's N rows.
+      const int rows = kPair ? mma_rows<kPair>(tile.rows) / 2 : tile.rows;
+      const int row0 = tile.row0 + (kPair ? static_cast<int>(rank) * rows : 0);
+      const int b = rows <= p.box[0] ? 0 : (rows <= p.box[1] ? 1 : 2);
+      const CUtensorMap* map = &maps.x[b];
       const uint32_t bytes = static_cast<uint32_t>(p.box[b]) * 128u;
       for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
         ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
@@ -314,103 +396,151 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
         if (!ok) break;
         if (ptx::elect_one()) {
           const uint32_t full = ptx::smem_addr(&bars->full[ring.s]);
-          ptx::mbar_arrive_expect_tx(full, bytes);
-          ptx::tma_load_2d(smem_base + ring.s * p.stage_bytes + kMx4BlockBytes, map, kb * 128, tile.row0, full, pol);
+          const uint32_t dst = smem_base + ring.s * p.stage_bytes + kMx4BlockBytes;
+          if constexpr (kPair) {
+            // The scales of all the tile's rows, in the tensor core's order, beside this CTA's half of the codes.
+            const uint32_t full0 = ptx::mapa(full, 0u);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(full, 2 * (bytes + kMx4XsTileBytes));
+            ptx::tma_load_2d_pair(dst, map, kb * 128, row0, full0, pol);
+            ptx::tma_load_2d_pair(dst + static_cast<uint32_t>(p.npad / 2) * 128u, &maps.xs_tiles, 0,
+                                  (tile.row_tile * p.kblocks + kb) * (kMx4XsTileBytes / 128), full0, pol);
+          } else {
+            ptx::mbar_arrive_expect_tx(full, bytes);
+            ptx::tma_load_2d(dst, map, kb * 128, row0, full, pol);
+          }
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (!kPair && warp == 8) {
     // ------------------------------------------------------------ activation scales in
+    // The words of one column group and neighbouring rows, as they lie in memory:
+    // one-dimensional boxes of 64 or 256 words from the last 16-byte boundary in
+    // front of the tile's first row (words past the array read as zeros).
     test_gate_wait();
-    ptx::griddep_wait();
-    TileWalker walk(p, list);
-    Ring ring(static_cast<uint32_t>(p.stages));
+    __syncwarp();
     bool ok = __all_sync(0xffffffffu, !*abort_flag);
+    ptx::griddep_wait();
+    const uint64_t pol = ptx::policy_evict_last();
+    TileWalker<kPair> walk(p, list);
+    Ring ring(kXsSlots);
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
       for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
-        ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
+        ok = wait_all(ptx::smem_addr(&bars->xs_empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
                       abort_flag);
         if (!ok) break;
-        const uint32_t dst = smem_base + ring.s * p.stage_bytes + p.xs_off + static_cast<uint32_t>(lane) * 4u;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int g = 2 * kb + j;
-          if (g >= p.groups) break;
-          const uint32_t* src = p.xs + static_cast<size_t>(g) * p.T + tile.row0;
-          for (int r = lane; r < tile.rows; r += 32)
-            ptx::cp_async4(dst + j * group_bytes + static_cast<uint32_t>(r - lane) * 4u, src + r);
+        if (ptx::elect_one()) {
+          const uint32_t dst = xs_base + ring.s * p.xs_bytes, bar = ptx::smem_addr(&bars->xs_in[ring.s]);
+          const int g0 = 2 * kb, g1 = min(2 * kb + 1, p.groups - 1);  // past the last group the last one again, unused
+          const int x0 = (g0 * p.T + tile.row0) & ~3, x1 = (g1 * p.T + tile.row0) & ~3;
+          const bool wide = tile.rows > 61;  // up to three words in front of the tile's rows
+          ptx::mbar_arrive_expect_tx(bar, wide ? 2048u : 512u);
+          const CUtensorMap* map = wide ? &maps.xs_wide : &maps.xs_narrow;
+          ptx::tma_load_1d(dst, map, x0, bar, pol);
+          ptx::tma_load_1d(dst + group_bytes, map, x1, bar, pol);
         }
-        ptx::cp_async_arrive(ptx::smem_addr(&bars->xs_in[ring.s]));
       }
     }
-  } else if (warp == 9) {
+  } else if (!kPair && warp == 9) {
     // ------------------------------------------------------------ activation scales into tcgen05.cp's order
-    // In place, 128 rows (512 bytes) at a time. A warp of its own: the fence in
-    // front of the tensor core's reads waits for the memory operations the warp
-    // has in flight, so in the loading warp it put one trip to L2 into every block.
-    const int my_tiles = unit < total ? (total - unit + units - 1) / units : 0;
-    const int items = my_tiles * (kb1 - kb0);
-    Ring ring(static_cast<uint32_t>(p.stages));
-    for (int i = 0; i < items; ++i, ring.advance()) {
-      if (!wait_all(ptx::smem_addr(&bars->xs_in[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
-                    abort_flag))
-        break;
-      const uint32_t base = smem_base + ring.s * p.stage_bytes + p.xs_off;
-      for (uint32_t a = 0; a < 2u * group_bytes; a += 512u) {
-        uint32_t w[4];
+    // A warp of its own: the fence in front of the tensor core's reads waits for
+    // the memory operations the warp has in flight. Lane l takes rows l, 32 + l, ..
+    // of both groups and writes them back as one 16-byte word per 128 rows.
+    TileWalker<kPair> walk(p, list);
+    Ring ring(kXsSlots);
+    bool ok = true;
+    for (int t = unit; ok && t < total; t += units) {
+      const Tile tile = walk.get(t);
+      for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
+        ok = wait_all(ptx::smem_addr(&bars->xs_in[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
+                      abort_flag);
+        if (!ok) break;
+        const uint32_t base = xs_base + ring.s * p.xs_bytes;
+        const uint32_t s0 = static_cast<uint32_t>(2 * kb * p.T + tile.row0) & 3u;
+        const uint32_t s1 = static_cast<uint32_t>(min(2 * kb + 1, p.groups - 1) * p.T + tile.row0) & 3u;
+        uint32_t w[2][8];
 #pragma unroll
-        for (uint32_t q = 0; q < 4; ++q) w[q] = ptx::ld_smem_u32(base + a + q * 128u + static_cast<uint32_t>(lane) * 4u);
+        for (uint32_t q = 0; q < 8; ++q) {
+          if (32 * static_cast<int>(q) >= tile.rows) break;
+          const uint32_t at = base + (32u * q + static_cast<uint32_t>(lane)) * 4u;
+          w[0][q] = ptx::ld_smem_u32(at + 4u * s0);
+          w[1][q] = ptx::ld_smem_u32(at + 4u * s1 + group_bytes);
+        }
         __syncwarp();
-        ptx::st_smem_u4(base + a + static_cast<uint32_t>(lane) * 16u, w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) {
+          const uint32_t dst = base + j * group_bytes + static_cast<uint32_t>(lane) * 16u;
+          ptx::st_smem_u4(dst, w[j][0], w[j][1], w[j][2], w[j][3]);
+          if (tile.rows > 128) ptx::st_smem_u4(dst + 512u, w[j][4], w[j][5], w[j][6], w[j][7]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&bars->xs_full[ring.s]));
       }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&bars->full[ring.s]));
     }
   } else if (warp == 4) {
     // ------------------------------------------------------------ MMA issue
     // The whole warp walks the blocks and one elected lane issues: with control
     // flow the compiler knows to be uniform, the operands stay in uniform
     // registers, where these instructions want them.
-    TileWalker walk(p, list);
-    Ring ring(static_cast<uint32_t>(p.stages));
+    TileWalker<kPair> walk(p, list);
+    Ring ring(static_cast<uint32_t>(p.stages)), xring(kXsSlots);
     const uint32_t sf_base = tmem_base + static_cast<uint32_t>(p.nacc * p.npad);
     const uint32_t atoms = (static_cast<uint32_t>(p.npad) + 127u) >> 7;
     uint32_t sbuf = 0, acc = 0, aph = 1;
-    bool ok = true;
+    bool ok = !(kPair && rank == 1);  // the even CTA issues the pair's MMAs
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
-      const uint32_t idesc = ptx::idesc_mxf4((static_cast<uint32_t>(tile.rows) + 15u) & ~15u, 0);
+      const uint32_t idesc = ptx::idesc_mxf4(static_cast<uint32_t>(mma_rows<kPair>(tile.rows)), 0, kPair ? 256u : 128u);
       const uint32_t sf2 = ptx::idesc_mxf4(0, 2) ^ ptx::idesc_mxf4(0, 0);
-      ok = wait_all(ptx::smem_addr(&bars->acc_empty[acc]), aph, p.status, SPENSE_DEVICE_TIMEOUT_MMA, abort_flag);
+      ok = wait_all<kPair>(ptx::smem_addr(&bars->acc_empty[acc]), aph, p.status, SPENSE_DEVICE_TIMEOUT_MMA, abort_flag);
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * static_cast<uint32_t>(p.npad);
-      for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
-        ok = wait_all(ptx::smem_addr(&bars->full[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_MMA, abort_flag);
+      for (int kb = kb0; kb < kb1; ++kb, ring.advance(), xring.advance()) {
+        ok = (kPair || wait_all(ptx::smem_addr(&bars->xs_full[xring.s]), xring.ph, p.status,
+                                SPENSE_DEVICE_TIMEOUT_MMA, abort_flag)) &&
+             wait_all(ptx::smem_addr(&bars->full[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_MMA, abort_flag);
         if (!ok) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint32_t a_s = smem_base + ring.s * p.stage_bytes;
           const uint64_t ad = ptx::desc_sw128(a_s), bd = ptx::desc_sw128(a_s + kMx4BlockBytes);
-          const uint64_t wd = ptx::desc_rows16(a_s + kMx4CodeBytes), xd = ptx::desc_rows16(a_s + p.xs_off);
+          const uint64_t wd = ptx::desc_rows16(a_s + kMx4CodeBytes), xd = ptx::desc_rows16(
+              kPair ? a_s + kMx4BlockBytes + static_cast<uint32_t>(p.npad / 2) * 128u : xs_base + xring.s * p.xs_bytes);
           // Scales: 8 columns for the weights' two column groups, then 8 a group for the activations.
           const uint32_t sfa = sf_base + sbuf * 24u, sfb = sfa + 8u;
           const uint32_t steps = kb + 1 == p.kblocks ? static_cast<uint32_t>(p.last_steps) : 4u;
+          auto cp = [](uint32_t taddr, uint64_t desc) {
+            if constexpr (kPair)
+              ptx::tmem_cp_32x128b_x4_pair(taddr, desc);
+            else
+              ptx::tmem_cp_32x128b_x4(taddr, desc);
+          };
+          auto commit = [](uint64_t* bar) {
+            if constexpr (kPair)
+              ptx::mma_commit_pair(ptx::smem_addr(bar), 0x3);
+            else
+              ptx::mma_commit(ptx::smem_addr(bar));
+          };
 #pragma unroll
           for (uint32_t j = 0; j < 2; ++j) {
-            ptx::tmem_cp_32x128b_x4(sfa + 4u * j, wd + 32u * j);
-            ptx::tmem_cp_32x128b_x4(sfb + 8u * j, xd + 32u * j * atoms);
-            if (atoms > 1) ptx::tmem_cp_32x128b_x4(sfb + 8u * j + 4u, xd + 32u * j * atoms + 32u);
+            cp(sfa + 4u * j, wd + 32u * j);
+            cp(sfb + 8u * j, xd + j * (group_bytes >> 4));
+            if (atoms > 1) cp(sfb + 8u * j + 4u, xd + j * (group_bytes >> 4) + 32u);
           }
+          if constexpr (!kPair) commit(&bars->xs_empty[xring.s]);
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
-            if (k < steps)
-              ptx::mma_mxf4(d_tmem, ad + 2u * k, bd + 2u * k, idesc ^ ((k & 1u) ? sf2 : 0u), sfa + 4u * (k >> 1),
-                            sfb + 8u * (k >> 1), (kb > kb0 || k > 0) ? 1u : 0u);
-          ptx::mma_commit(ptx::smem_addr(&bars->empty[ring.s]));
-          if (kb + 1 == kb1) ptx::mma_commit(ptx::smem_addr(&bars->acc_full[acc]));
+          for (uint32_t k = 0; k < 4; ++k) {
+            if (k >= steps) break;
+            const uint32_t id = idesc ^ ((k & 1u) ? sf2 : 0u), accum = (kb > kb0 || k > 0) ? 1u : 0u;
+            if constexpr (kPair)
+              ptx::mma_mxf4_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, sfa + 4u * (k >> 1), sfb + 8u * (k >> 1), accum);
+            else
+              ptx::mma_mxf4(d_tmem, ad + 2u * k, bd + 2u * k, id, sfa + 4u * (k >> 1), sfb + 8u * (k >> 1), accum);
+          }
+          commit(&bars->empty[ring.s]);
+          if (kb + 1 == kb1) commit(&bars->acc_full[acc]);
         }
         __syncwarp();
         sbuf ^= 1u;
@@ -420,10 +550,10 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
         aph ^= 1u;
       }
     }
-  } else {
+  } else if (warp < 4) {
     // ------------------------------------------------------------ epilogue
     ptx::griddep_wait();  // Y may be the previous grid's
-    TileWalker walk(p, list);
+    TileWalker<kPair> walk(p, list);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
     int u = 0;
     for (int t = unit; t < total; t += units, ++u) {
@@ -435,49 +565,65 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
         break;
       ptx::tc_fence_after();
       const uint32_t taddr = lane_base + acc * static_cast<uint32_t>(p.npad);
-      const int n_warp = tile.n_tile * kMx4Rows + warp * 32;
+      const int n_warp = (kPair ? 2 * tile.n_tile + static_cast<int>(rank) : tile.n_tile) * kMx4Rows + warp * 32;
       uint16_t* const y = p.y + static_cast<int64_t>(tile.row0) * p.ldy;
-      if (p.split > 1) break;  // finished below, with the other CTAs of the cluster
-      for (int c0 = 0; c0 < tile.rows; c0 += 16) {
-        uint32_t v[16];
-        ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c0), v);
+      if (split) break;  // finished below, with the other CTAs of the cluster
+      // The next 32 rows are read while the ones before are stored.
+      uint32_t v[32], next[32];
+      ptx::tmem_ld_32x32b_x32(taddr, next);
+      for (int c0 = 0; c0 < tile.rows; c0 += 32) {
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t q[4];
+        for (int i = 0; i < 32; ++i) v[i] = next[i];
+        if (c0 + 32 < tile.rows) ptx::tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c0 + 32), next);
+        float a[32];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            q[j] = bf16x2(__uint_as_float(v[8 * h + 2 * j]), __uint_as_float(v[8 * h + 2 * j + 1]));
-          store_8rows(q, lane, y, p.ldy, c0 + 8 * h, tile.rows, n_warp, p.N);
-        }
+        for (int i = 0; i < 32; ++i) a[i] = __uint_as_float(v[i]);
+        if (tile.rows - c0 <= 8)
+          store_rows<1>(a, lane, y, p.ldy, c0, tile.rows, n_warp, p.N);
+        else
+          store_rows<4>(a, lane, y, p.ldy, c0, tile.rows, n_warp, p.N);
       }
       ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_addr(&bars->acc_empty[acc]));
+      if (kPair && rank == 1) {
+        ptx::named_bar_sync(1, 128);
+        if (threadIdx.x == 0)
+          ptx::mbar_arrive_remote_release(ptx::mapa(ptx::smem_addr(&bars->acc_empty[acc]), 0u));
+      } else {
+        ptx::mbar_arrive(ptx::smem_addr(&bars->acc_empty[acc]));
+      }
     }
   }
   __syncwarp();
-  if (p.split > 1) {
-    // One tile a cluster at most. Every thread of the cluster meets here: every
-    // MMA of the cluster has completed, so rank 0's ring is idle and takes the
-    // peers' partials, [rank - 1][row / 4][128 weight rows][4 rows].
+  if (split) {
+    // One tile a cluster at most. The CTAs finish a share of its rows each: `chunk`
+    // rows from rank * chunk on. Every thread of the cluster meets here twice: when
+    // all MMAs of the cluster have completed, so that every ring is idle and takes
+    // the others' partials of its CTA's rows ([source][row / 4][128 weight rows][4
+    // rows]), and when they are all in.
     ptx::tc_fence_before();
-    ptx::cluster_arrive();
+    ptx::cluster_arrive_relaxed();
     ptx::cluster_wait();
     ptx::tc_fence_after();
     const bool work = warp < 4 && unit < total && !*abort_flag;
-    TileWalker walk(p, list);
-    const Tile tile = work ? walk.get(unit) : Tile{0, 0, 0, 0};
+    TileWalker<kPair> walk(p, list);
+    const Tile tile = work ? walk.get(unit) : Tile{0, 0, 0, 0, 0};
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-    if (work && rank != 0) {
-      const uint32_t dst = ptx::mapa(smem_base + (rank - 1u) * static_cast<uint32_t>(p.npad) * 512u +
-                                         static_cast<uint32_t>(warp * 32 + lane) * 16u, 0u);
-      for (int c0 = 0; c0 < tile.rows; c0 += 16) {
-        uint32_t v[16];
-        ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c0), v);
+    const int me = static_cast<int>(rank);
+    const int chunk = ((tile.rows + p.split - 1) / p.split + 7) & ~7;
+    const uint32_t at = smem_base + static_cast<uint32_t>(warp * 32 + lane) * 16u;
+    for (int o = 1; work && o < p.split; ++o) {
+      const int r = me + o < p.split ? me + o : me + o - p.split;  // the owner; each source starts with another
+      const int r0 = r * chunk, r1 = min(tile.rows, r0 + chunk);
+      const uint32_t dst =
+          ptx::mapa(at + static_cast<uint32_t>((me < r ? me : me - 1) * chunk) * 512u, static_cast<uint32_t>(r));
+      for (int c0 = r0; c0 < r1; c0 += 8) {
+        uint32_t v[8];
+        ptx::tmem_ld_32x32b_x8(taddr + static_cast<uint32_t>(c0), v);
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          ptx::st_cluster_v4(dst + static_cast<uint32_t>(c0 / 4 + q) * 2048u,
+        for (int q = 0; q < 2; ++q)
+          ptx::st_cluster_v4(dst + static_cast<uint32_t>((c0 - r0) / 4 + q) * 2048u,
                              make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
                                          __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])));
       }
@@ -485,35 +631,38 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
     __syncwarp();
     ptx::cluster_arrive();
     ptx::cluster_wait();
-    if (work && rank == 0) {
+    if (work) {
       const int n_warp = tile.n_tile * kMx4Rows + warp * 32;
       uint16_t* const y = p.y + static_cast<int64_t>(tile.row0) * p.ldy;
-      const uint32_t src = smem_base + static_cast<uint32_t>(warp * 32 + lane) * 16u;
-      for (int c0 = 0; c0 < tile.rows; c0 += 16) {
-        uint32_t v[16];
-        ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c0), v);
+      const int r0 = me * chunk, r1 = min(tile.rows, r0 + chunk);
+      for (int c0 = r0; c0 < r1; c0 += 8) {
+        uint32_t v[8];
+        ptx::tmem_ld_32x32b_x8(taddr + static_cast<uint32_t>(c0), v);
         ptx::tmem_ld_wait();
-        float a[16];
+        float a[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] = __uint_as_float(v[i]);
-        for (int r = 1; r < p.split; ++r) {
-          const uint32_t s = src + static_cast<uint32_t>(r - 1) * static_cast<uint32_t>(p.npad) * 512u;
+        for (int i = 0; i < 8; ++i) a[i] = 0.0f;
+        for (int r = 0; r < p.split; ++r) {  // in rank order, this CTA's own sums among them
+          float4 f[2];
+          if (r == me) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 f = ptx::ld_smem_v4(s + static_cast<uint32_t>(c0 / 4 + q) * 2048u);
-            a[4 * q] += f.x;
-            a[4 * q + 1] += f.y;
-            a[4 * q + 2] += f.z;
-            a[4 * q + 3] += f.w;
+            for (int q = 0; q < 2; ++q)
+              f[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                 __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+          } else {
+            const uint32_t src = at + static_cast<uint32_t>((r < me ? r : r - 1) * chunk) * 512u;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) f[q] = ptx::ld_smem_v4(src + static_cast<uint32_t>((c0 - r0) / 4 + q) * 2048u);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            a[4 * q] += f[q].x;
+            a[4 * q + 1] += f[q].y;
+            a[4 * q + 2] += f[q].z;
+            a[4 * q + 3] += f[q].w;
           }
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t q[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) q[j] = bf16x2(a[8 * h + 2 * j], a[8 * h + 2 * j + 1]);
-          store_8rows(q, lane, y, p.ldy, c0 + 8 * h, tile.rows, n_warp, p.N);
-        }
+        store_rows<1>(a, lane, y, p.ldy, c0, tile.rows, n_warp, p.N);
       }
     }
   }
@@ -523,44 +672,142 @@ __global__ void __launch_bounds__(kMx4Threads, 2)
     const uint64_t t0 = ptx::globaltimer();
     while (ptx::globaltimer() - t0 < 2000000ull) __nanosleep(1000);
   }
+  if (kPair && rank == 1 && warp == 0 && lane == 0) {
+    // The even CTA's completion signals land in this CTA's stage barriers
+    // asynchronously: wait (bounded) for the last one of every stage. After a
+    // failure they may never come; the wait runs out.
+    const int my_tiles = unit < total ? (total - unit + units - 1) / units : 0;
+    const int items = my_tiles * (kb1 - kb0);
+    const uint64_t t0 = ptx::globaltimer();
+    for (int i = items > p.stages ? items - p.stages : 0; i < items; ++i) {
+      const uint32_t bar = ptx::smem_addr(&bars->empty[i % p.stages]);
+      while (!ptx::mbar_try_wait(bar, static_cast<uint32_t>((i / p.stages) & 1)) &&
+             ptx::globaltimer() - t0 < kWaitLimitNs) {
+      }
+    }
+  }
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 4) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, p.tmem_cols);
+    if constexpr (kPair)
+      ptx::tmem_dealloc_pair(tmem_base, p.tmem_cols);
+    else
+      ptx::tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+  if (kPair) {
+    // Neither CTA of a pair leaves while the other may still signal into it.
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+  }
+}
+
+// Pair mode's activation scales: for every row tile and block, the image warp 9
+// makes of them in the other mode, so that the pair needs no generic write to
+// shared memory that the other CTA's tensor instructions have to see (a release
+// at cluster scope took 0.8 us a block). One CTA a row tile and 16 blocks.
+constexpr int kTileThreads = 256;
+constexpr int kTileBlocks = 16;
+
+__global__ void __launch_bounds__(kTileThreads)
+    mx4_scale_tiles_kernel(const uint32_t* __restrict__ xs, const int32_t* __restrict__ offsets, int E, int T, int npad,
+                           int groups, int kblocks, uint32_t* __restrict__ out) {
+  ptx::griddep_launch_dependents();
+  __shared__ int found[2];
+  const int spans = (kblocks + kTileBlocks - 1) / kTileBlocks;
+  const int rt = static_cast<int>(blockIdx.x) / spans, kb0 = (static_cast<int>(blockIdx.x) - rt * spans) * kTileBlocks;
+  if (threadIdx.x < 2) found[threadIdx.x] = 0;
+  ptx::griddep_wait();
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int begin = 0, carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      int lo, hi;
+      expert_rows(offsets, E, T, e0, lane, carry, lo, hi);
+      const int tiles = (hi - lo + npad - 1) / npad;
+      const int scan = warp_scan(tiles, lane);
+      const int first = begin + scan - tiles;
+      if (rt >= first && rt < first + tiles) {
+        found[0] = lo + (rt - first) * npad;
+        found[1] = min(npad, hi - found[0]);
+      }
+      begin += __shfl_sync(0xffffffffu, scan, 31);
+    }
+  }
+  __syncthreads();
+  const int row0 = found[0], rows = found[1], r = threadIdx.x;
+  if (rows == 0) return;  // past the last row tile
+  uint32_t* dst = out + (static_cast<size_t>(rt) * kblocks + kb0) * (kMx4XsTileBytes / 4) + (r >> 7) * 128 +
+                  (r & 31) * 4 + ((r >> 5) & 3);
+#pragma unroll 4
+  for (int i = 0; i < 2 * kTileBlocks; ++i) {
+    const int g = 2 * kb0 + i;
+    if (g >= 2 * kblocks) break;
+    dst[i * 256] = r < rows && g < groups ? __ldg(xs + static_cast<size_t>(g) * T + row0 + r) : 0u;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_mx4_gemm(const CUtensorMap (&maps)[3], const Mx4GemmParams& p, int grid, uint32_t smem_bytes,
-                            cudaStream_t stream) {
+cudaError_t launch_mx4_scale_tiles(const Mx4GemmParams& p, int row_tiles, uint32_t* out, cudaStream_t stream) {
+  const int spans = (p.kblocks + kTileBlocks - 1) / kTileBlocks;
+  return launch_pdl(mx4_scale_tiles_kernel, static_cast<unsigned int>(row_tiles * spans), kTileThreads, 0, stream, p.xs,
+                    p.offsets, p.E, p.T, p.npad, p.groups, p.kblocks, out);
+}
+
+namespace {
+
+cudaError_t allow_smem() {
   static thread_local int configured_for = -1;
   int dev = 0;
   cudaError_t st = cudaGetDevice(&dev);
-  if (st != cudaSuccess) return st;
-  if (configured_for != dev) {
-    st = cudaFuncSetAttribute(spense_mx4_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-    if (st != cudaSuccess) return st;
-    configured_for = dev;
-  }
+  if (st != cudaSuccess || configured_for == dev) return st;
+  st = cudaFuncSetAttribute(spense_mx4_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (st == cudaSuccess)
+    st = cudaFuncSetAttribute(spense_mx4_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (st == cudaSuccess) configured_for = dev;
+  return st;
+}
+
+cudaLaunchConfig_t gemm_config(int grid, int cluster, uint32_t smem_bytes, cudaStream_t stream,
+                               cudaLaunchAttribute (&attr)[3]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned int>(grid));
   cfg.blockDim = dim3(kMx4Threads);
   cfg.dynamicSmemBytes = smem_bytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned int>(p.split);
+  attr[1].val.clusterDim.x = static_cast<unsigned int>(cluster);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   attr[2].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
   attr[2].val.clusterSchedulingPolicyPreference = cudaClusterSchedulingPolicyLoadBalancing;
   cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 3 : 1;
-  return cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel, maps[0], maps[1], maps[2], p);
+  cfg.numAttrs = cluster > 1 ? 3 : 1;
+  return cfg;
+}
+
+}  // namespace
+
+cudaError_t mx4_max_clusters(int cluster, uint32_t smem_bytes, int* out) {
+  cudaError_t st = allow_smem();
+  if (st != cudaSuccess) return st;
+  cudaLaunchAttribute attr[3];
+  const cudaLaunchConfig_t cfg = gemm_config(cluster, cluster, smem_bytes, nullptr, attr);
+  return cudaOccupancyMaxActiveClusters(out, spense_mx4_gemm_kernel<false>, &cfg);
+}
+
+cudaError_t launch_mx4_gemm(const Mx4GemmMaps& maps, const Mx4GemmParams& p, int grid, uint32_t smem_bytes,
+                            cudaStream_t stream) {
+  const cudaError_t st = allow_smem();
+  if (st != cudaSuccess) return st;
+  cudaLaunchAttribute attr[3];
+  const cudaLaunchConfig_t cfg = gemm_config(grid, p.pair ? 2 : p.split, smem_bytes, stream, attr);
+  return p.pair ? cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<true>, maps, p)
+                : cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<false>, maps, p);
 }
 
 }  // namespace spense

@@ -19,6 +19,8 @@ constexpr int kMx4ScaleBytes = 1024;
 constexpr int kMx4BlockBytes = kMx4CodeBytes + kMx4ScaleBytes;
 
 constexpr int kMx4BarrierBytes = 512;  // mbarriers and flags behind the ring
+constexpr int kMx4XsSlots = 8;  // blocks whose activation scales are ahead of the products
+constexpr int kMx4XsTileBytes = 2048;  // scales of a block for up to 256 rows, in tcgen05.cp's order
 constexpr int kMx4MaxExperts = 1024;
 constexpr int64_t kMx4MaxRows = 1 << 20;
 
@@ -34,20 +36,38 @@ struct Mx4GemmParams {
   int n_tiles, kblocks, groups;
   int last_steps;          // K = 64 steps in the last block (1 .. 4)
   int npad;                // rows of activations per tile (MMA N), a multiple of 16
-  int box[3];              // rows one activation load covers, smallest first; box[2] == npad
+  int box[3];              // rows one activation load covers, smallest first; box[2]: a CTA's share of npad
   int stages, nacc;
+  int pair;                // 1: CTA pairs (tcgen05 cta_group::2) share 256-row MMAs
   int split;               // CTAs of a cluster sharing one tile's K range (1: none)
-  uint32_t stage_bytes, xs_off, tmem_cols;
+  uint32_t stage_bytes, xs_bytes, tmem_cols;  // bytes of a stage, of a slot of activation scales
   int w_keep;              // 1: weights are read again by later tiles, keep them in L2
 };
 
-struct Mx4GemmPlan {
-  int npad, stages, nacc, split, ctas_per_sm, grid;
-  uint32_t stage_bytes, xs_off, tmem_cols, smem_bytes;
+// Tensor maps of a launch: the activation codes in three box heights, and the
+// scale words as one array in boxes of 64 and 256 words.
+struct Mx4GemmMaps {
+  CUtensorMap x[3];
+  CUtensorMap xs_narrow, xs_wide;
+  CUtensorMap w, xs_tiles;  // pair mode: the packed blocks and the scale tiles, as rows of 128 bytes
 };
 
-cudaError_t launch_mx4_gemm(const CUtensorMap (&maps)[3], const Mx4GemmParams& p, int grid, uint32_t smem_bytes,
+constexpr int kMx4MaxTile = 240;  // rows a tile takes: with three words in front, one box of 256 scale words
+
+struct Mx4GemmPlan {
+  int npad, stages, nacc, pair, split, ctas_per_sm, grid;
+  int64_t row_tiles;  // row tiles at most (all experts)
+  size_t workspace_bytes;
+  uint32_t stage_bytes, xs_bytes, tmem_cols, smem_bytes;
+};
+
+cudaError_t launch_mx4_gemm(const Mx4GemmMaps& maps, const Mx4GemmParams& p, int grid, uint32_t smem_bytes,
                             cudaStream_t stream);
+
+// Clusters of `cluster` CTAs with that much shared memory the device holds at once.
+cudaError_t mx4_max_clusters(int cluster, uint32_t smem_bytes, int* out);
+// Pair mode: the activation scales of p's row tiles in tcgen05.cp's order.
+cudaError_t launch_mx4_scale_tiles(const Mx4GemmParams& p, int row_tiles, uint32_t* out, cudaStream_t stream);
 
 // x_type: SPENSE_TYPE_*. rows: gather index [T] or NULL. words: scales as words.
 cudaError_t launch_mx4_quantize(const void* X, int x_type, int64_t T, int64_t K, int64_t ldx, const int32_t* rows,

@@ -554,9 +554,10 @@ SPENSE_API spense_status spense_mx4_gemm(const spense_mx4_packed* Wp, const uint
  * spense_mx4_gemm_experts — the same product grouped by expert: for every expert
  * e, rows offsets[e] .. offsets[e + 1] of X with weight e.
  *   T        rows of X, x_scale (its layout's R) and Y.
- *   offsets  device int32 [E + 1], ascending, within [0, T] (others are cut to
- *            that; read on the device only, so nothing is synchronized). An
- *            expert may have no rows.
+ *   offsets  device int32 [E + 1], ascending, within [0, T] (read on the device
+ *            only, so nothing is synchronized; values outside [0, T] are cut to it,
+ *            and one below an earlier one counts as that). An expert may have no
+ *            rows.
  * Rows outside every expert's range (behind offsets[E], say) are left as they
  * were in Y. Other arguments and errors as spense_mx4_gemm.
  */
