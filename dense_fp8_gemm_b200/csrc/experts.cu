@@ -15,14 +15,16 @@ namespace {
 // A counting sort: position of choice i = (choices of smaller experts) +
 // (earlier choices of the same expert). The choices are cut into chunks of one
 // CTA each, and a chunk into 32 contiguous runs of one warp each; a warp takes
-// its run 32 choices at a time and finds the equal ones among them with one
-// match instruction, so nothing depends on the order in which warps or CTAs
+// its run 32 choices at a time and finds the equal ones among them by ballots, so nothing depends on the order in which warps or CTAs
 // arrive and the result is the stable one.
 //   kSingle  the one chunk: counts, offsets and positions in one launch.
-//   kCount   counts of a chunk into counts[chunk][E].
-//   kPlace   recounts the chunk, takes its bases from all chunks' counts.
+//   kCount   counts of a chunk into counts[E][chunks].
+//   kPlace   recounts the chunk and takes its bases from all chunks' counts, a
+//            warp an expert at a time, so that they are read in whole lines (one
+//            thread an expert took 18.4 us for 131072 choices of 256 experts).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kKept = 4;  // rounds of 32 choices a warp keeps in registers
 enum SortMode { kSingle, kCount, kPlace };
 
 template <bool kWide>
@@ -37,13 +39,28 @@ __device__ __forceinline__ int expert_of(const void* ids, int i, int end, int E)
   }
 }
 
+// Lanes with the same expert, by its bits: one ballot each. (The match instruction
+// goes through the different values one by one: 4096 choices of 128 experts took
+// 11.7 us with it.)
+__device__ __forceinline__ uint32_t lanes_with(int e, int bits) {
+  uint32_t same = 0xffffffffu;
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (e >> b) & 1;
+    const uint32_t v = __ballot_sync(0xffffffffu, set);
+    same &= set ? v : ~v;
+  }
+  return same;
+}
+
 template <bool kWide, SortMode kMode>
 __global__ void __launch_bounds__(kSortThreads)
-    expert_sort_kernel(const void* __restrict__ ids, int n, int k, int E, int chunk, int32_t* __restrict__ offsets,
+    expert_sort_kernel(const void* __restrict__ ids, int n, int k, int E, int bits, int chunk,
+                       int32_t* __restrict__ offsets,
                        int32_t* __restrict__ rows, int32_t* __restrict__ pos, int32_t* __restrict__ counts) {
   extern __shared__ int hist[];  // [warps][E]: the warp's choices of an expert, then its first position
   __shared__ int warp_sum[kSortWarps];
   __shared__ int total_live;
+  const int stride = (gridDim.x + 3) & ~3;  // of counts, so that four are 16 bytes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t below = (1u << lane) - 1u;
   pdl_trigger();
@@ -54,36 +71,79 @@ __global__ void __launch_bounds__(kSortThreads)
   const int run = ((chunk + kSortThreads - 1) / kSortThreads) * 32;
   const int i0 = min(c1, c0 + warp * run), i1 = min(c1, i0 + run);
   int* const mine = hist + warp * E;
-  for (int b = i0; b < i1; b += 32) {
-    const int e = expert_of<kWide>(ids, b + lane, i1, E);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
+  // The run's first kKept rounds stay in registers for the second pass.
+  int kept[kKept];
+  uint32_t kept_same[kKept];
+#pragma unroll
+  for (int q = 0; q < kKept; ++q) kept[q] = expert_of<kWide>(ids, i0 + 32 * q + lane, i1, E);
+#pragma unroll
+  for (int q = 0; q < kKept; ++q) kept_same[q] = i0 + 32 * q < i1 ? lanes_with(kept[q], bits) : 0u;
+  auto count = [&](int e, uint32_t same) {
     if (e < E && (same & below) == 0u) mine[e] += __popc(same);
     __syncwarp();
+  };
+#pragma unroll
+  for (int q = 0; q < kKept; ++q)
+    if (i0 + 32 * q < i1) count(kept[q], kept_same[q]);
+  for (int b = i0 + 32 * kKept; b < i1; b += 32) {
+    const int e = expert_of<kWide>(ids, b + lane, i1, E);
+    count(e, lanes_with(e, bits));
   }
   __syncthreads();
   // Thread t: the expert t (E <= 1024). Its choices in this chunk, and before it.
   const int t = threadIdx.x;
+  const int warps = min(kSortWarps, (c1 - c0 + run - 1) / run);  // with choices
   int sum = 0, before = 0;
   if (t < E) {
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = hist[w * E + t];
-      hist[w * E + t] = sum;
-      sum += c;
+    for (int w0 = 0; w0 < warps; w0 += 8) {  // eight reads in flight (a warp without choices counted none)
+      int c[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) c[w] = hist[(w0 + w) * E + t];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        hist[(w0 + w) * E + t] = sum;
+        sum += c[w];
+      }
     }
   }
   if constexpr (kMode == kCount) {
-    if (t < E) counts[blockIdx.x * E + t] = sum;
+    if (t < E) counts[t * stride + blockIdx.x] = sum;
     return;
   }
   int total = sum;
   if constexpr (kMode == kPlace) {
-    total = 0;
-    if (t < E)
-      for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
-        const int v = __ldcg(counts + c * E + t);
-        if (c < static_cast<int>(blockIdx.x)) before += v;
-        total += v;
+    __shared__ int2 bases[kMx4MaxExperts];
+    // A lane takes four chunks' counts (there are 128 chunks at most), a warp four
+    // experts at a time.
+    const int chunks = static_cast<int>(gridDim.x), c = 4 * lane;
+    for (int e0 = warp; e0 < E; e0 += 4 * kSortWarps) {
+      int4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + u * kSortWarps;
+        v[u] = make_int4(0, 0, 0, 0);
+        if (e < E && c < chunks) v[u] = __ldcg(reinterpret_cast<const int4*>(counts + e * stride + c));
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + u * kSortWarps;
+        const int w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        int all = 0, less = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          all += c + q < chunks ? w[q] : 0;
+          less += c + q < static_cast<int>(blockIdx.x) ? w[q] : 0;
+        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        less = __reduce_add_sync(0xffffffffu, less);
+        if (lane == 0 && e < E) bases[e] = make_int2(all, less);
+      }
+    }
+    __syncthreads();
+    if (t < E) {
+      total = bases[t].x;
+      before = bases[t].y;
+    }
   }
   // Exclusive scan of the experts' totals: the offsets.
   int scan = total;
@@ -108,14 +168,17 @@ __global__ void __launch_bounds__(kSortThreads)
   const int first = scan - total + (warp > 0 ? warp_sum[warp - 1] : 0);
   if (t < E) {
     if (blockIdx.x == 0) offsets[t] = first;
-    for (int w = 0; w < kSortWarps; ++w) hist[w * E + t] += first + before;
+    for (int w0 = 0; w0 < warps; w0 += 8) {
+      int c[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) c[w] = hist[(w0 + w) * E + t];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) hist[(w0 + w) * E + t] = c[w] + first + before;
+    }
   }
   if (blockIdx.x == 0 && t == 0) offsets[E] = total_live;
   __syncthreads();
-  for (int b = i0; b < i1; b += 32) {
-    const int i = b + lane;
-    const int e = expert_of<kWide>(ids, i, i1, E);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
+  auto place = [&](int i, int e, uint32_t same) {
     const uint32_t earlier = same & below;
     int p = -1;
     if (e < E) p = mine[e] + __popc(earlier);
@@ -126,6 +189,13 @@ __global__ void __launch_bounds__(kSortThreads)
       pos[i] = p;
       if (p >= 0) rows[p] = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(k));
     }
+  };
+#pragma unroll
+  for (int q = 0; q < kKept; ++q)
+    if (i0 + 32 * q < i1) place(i0 + 32 * q + lane, kept[q], kept_same[q]);
+  for (int b = i0 + 32 * kKept; b < i1; b += 32) {
+    const int e = expert_of<kWide>(ids, b + lane, i1, E);
+    place(b + lane, e, lanes_with(e, bits));
   }
   // The slots behind the last expert's (as many as there are choices left out).
   for (int i = total_live + blockIdx.x * kSortThreads + t; i < n; i += gridDim.x * kSortThreads) rows[i] = -1;
@@ -137,33 +207,37 @@ __global__ void __launch_bounds__(kSortThreads)
 // looked at). Bound by the gathered rows' bytes.
 constexpr int kCombineThreads = 128;
 
-__device__ __forceinline__ void fma8(float (&acc)[8], const uint4& v, float w) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    acc[2 * i] = fmaf(w, __uint_as_float(u[i] << 16), acc[2 * i]);
-    acc[2 * i + 1] = fmaf(w, __uint_as_float(u[i] & 0xFFFF0000u), acc[2 * i + 1]);
-  }
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// kVec: eight columns a thread (rows 16-byte aligned); else one.
+// Four bf16 values from element `at` on, which may lie on a 2-byte boundary only:
+// the aligned words around them, shifted together. (Never the last four of a row:
+// the word behind the array's last element is not read.)
+__device__ __forceinline__ uint2 load4(const uint16_t* Y, int64_t at) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(Y) + (at >> 1);
+  uint2 v = make_uint2(__ldg(w), __ldg(w + 1));
+  if (at & 1) v = make_uint2(__funnelshift_r(v.x, v.y, 16), __funnelshift_r(v.y, __ldg(w + 2), 16));
+  return v;
+}
+
+// kVec: eight columns a thread (rows 16-byte aligned). Else four, read as words on
+// any 2-byte boundary; the threads at a row's end read single values.
 template <bool kVec>
 __global__ void __launch_bounds__(kCombineThreads)
     expert_combine_kernel(const uint16_t* __restrict__ Y, int64_t T, int64_t N, int64_t ldy,
                           const int32_t* __restrict__ pos, const float* __restrict__ weights, int k,
                           uint16_t* __restrict__ out, int64_t ldo) {
-  constexpr int kCols = kVec ? 8 : 1;
+  constexpr int kCols = kVec ? 8 : 4;
   pdl_trigger();
-  const int64_t spans = (N + kCombineThreads * kCols - 1) / (kCombineThreads * kCols);
-  const int64_t m = blockIdx.x / spans;
-  const int64_t n = (blockIdx.x - m * spans) * (kCombineThreads * kCols) + threadIdx.x * kCols;
+  const unsigned int spans = static_cast<unsigned int>((N + kCombineThreads * kCols - 1) / (kCombineThreads * kCols));
+  const unsigned int mb = blockIdx.x / spans;
+  const int64_t m = mb;
+  const int64_t n = (blockIdx.x - mb * spans) * (kCombineThreads * kCols) + threadIdx.x * kCols;
   pdl_wait();
   if (n >= N) return;
+  const bool whole = kVec || n + kCols < N;
   float acc[kCols];
 #pragma unroll
   for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
@@ -172,47 +246,78 @@ __global__ void __launch_bounds__(kCombineThreads)
   for (int j0 = 0; j0 < k; j0 += 8) {
     float w[8];
     bool live[8];
-    uint4 v[kVec ? 8 : 1];
-    uint16_t s[kVec ? 1 : 8];
+    uint4 v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       live[j] = false;
+      w[j] = 0.0f;
+      v[j] = make_uint4(0u, 0u, 0u, 0u);
       if (j0 + j < k) {
         const int64_t p = __ldg(pm + j0 + j);
         live[j] = p >= 0 && p < T;
         if (live[j]) {
           w[j] = __ldg(wm + j0 + j);
-          if constexpr (kVec)
+          if constexpr (kVec) {
             v[j] = __ldg(reinterpret_cast<const uint4*>(Y + p * ldy + n));
-          else
-            s[j] = __ldg(Y + p * ldy + n);
+          } else if (whole) {
+            const uint2 u = load4(Y, p * ldy + n);
+            v[j].x = u.x;
+            v[j].y = u.y;
+          } else {
+            const uint16_t* s = Y + p * ldy + n;
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = n + i < N ? __ldg(s + i) : 0u;
+            v[j].x = h[0] | (h[1] << 16);
+            v[j].y = h[2] | (h[3] << 16);
+          }
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (live[j]) {
-        if constexpr (kVec)
-          fma8(acc, v[j], w[j]);
-        else
-          acc[0] = fmaf(w[j], __uint_as_float(static_cast<uint32_t>(s[j]) << 16), acc[0]);
+    for (int j = 0; j < 8; ++j) {
+      if (!live[j]) continue;
+      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) {
+        acc[2 * i] = fmaf(w[j], __uint_as_float(u[i] << 16), acc[2 * i]);
+        acc[2 * i + 1] = fmaf(w[j], __uint_as_float(u[i] & 0xFFFF0000u), acc[2 * i + 1]);
       }
+    }
   }
+  uint16_t* o = out + m * ldo + n;
   if constexpr (kVec) {
-    *reinterpret_cast<uint4*>(out + m * ldo + n) = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
-                                                              pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
+    *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
+                                              pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
   } else {
-    out[m * ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
+    const uint32_t lo = pack_bf16(acc[0], acc[1]), hi = pack_bf16(acc[2], acc[3]);
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) o[i] = static_cast<uint16_t>((i < 2 ? lo : hi) >> (16 * (i & 1)));
+    } else if ((reinterpret_cast<uintptr_t>(o) & 2) == 0) {
+      reinterpret_cast<uint32_t*>(o)[0] = lo;
+      reinterpret_cast<uint32_t*>(o)[1] = hi;
+    } else {
+      o[0] = static_cast<uint16_t>(lo);
+      *reinterpret_cast<uint32_t*>(o + 1) = __byte_perm(lo, hi, 0x5432);
+      o[3] = static_cast<uint16_t>(hi >> 16);
+    }
   }
 }
 
-constexpr int kSortMinChunk = 4096;  // one chunk (one launch) up to here
+// One chunk (one launch) up to 4096 choices (7.1 us there either way), else chunks of
+// 1024 while there are at most 128 of them: 131072 choices of 256 experts in 10.7 us,
+// in chunks of 4096 some 4 us more.
+constexpr int kSortMinChunk = 4096;
 constexpr int kSortMaxChunks = 128;
 
 int64_t sort_chunk(int64_t n) {
   if (n <= kSortMinChunk) return n < 1 ? 1 : n;
   return std::max<int64_t>(kSortThreads, ((n + kSortMaxChunks - 1) / kSortMaxChunks + 1023) / 1024 * 1024);
 }
+
+int64_t expert_sort_chunks(int64_t n) { return n < 1 ? 1 : (n + sort_chunk(n) - 1) / sort_chunk(n); }
 
 template <bool kWide>
 cudaError_t sort_typed(const void* ids, int64_t n, int k, int E, int32_t* offsets, int32_t* rows, int32_t* pos,
@@ -234,19 +339,21 @@ cudaError_t sort_typed(const void* ids, int64_t n, int k, int E, int32_t* offset
   const unsigned int grid = static_cast<unsigned int>(expert_sort_chunks(n));
   const size_t smem = static_cast<size_t>(kSortWarps) * E * 4;
   const int ni = static_cast<int>(n);
+  int bits = 1;
+  while ((E >> bits) != 0) ++bits;  // ids 0 .. E, E for the ones left out
   if (grid == 1)
-    return launch_pdl(expert_sort_kernel<kWide, kSingle>, 1u, kSortThreads, smem, stream, ids, ni, k, E, chunk,
+    return launch_pdl(expert_sort_kernel<kWide, kSingle>, 1u, kSortThreads, smem, stream, ids, ni, k, E, bits, chunk,
                       offsets, rows, pos, counts);
-  st = launch_pdl(expert_sort_kernel<kWide, kCount>, grid, kSortThreads, smem, stream, ids, ni, k, E, chunk, offsets,
+  st = launch_pdl(expert_sort_kernel<kWide, kCount>, grid, kSortThreads, smem, stream, ids, ni, k, E, bits, chunk, offsets,
                   rows, pos, counts);
   if (st != cudaSuccess) return st;
-  return launch_pdl(expert_sort_kernel<kWide, kPlace>, grid, kSortThreads, smem, stream, ids, ni, k, E, chunk, offsets,
+  return launch_pdl(expert_sort_kernel<kWide, kPlace>, grid, kSortThreads, smem, stream, ids, ni, k, E, bits, chunk, offsets,
                     rows, pos, counts);
 }
 
 }  // namespace
 
-int64_t expert_sort_chunks(int64_t n) { return n < 1 ? 1 : (n + sort_chunk(n) - 1) / sort_chunk(n); }
+int64_t expert_sort_counts(int64_t n, int64_t E) { return (expert_sort_chunks(n) + 3) / 4 * 4 * E; }
 
 cudaError_t launch_expert_sort(const void* ids, bool wide, int64_t n, int k, int E, int32_t* offsets, int32_t* rows,
                                int32_t* pos, int32_t* counts, cudaStream_t stream) {
@@ -259,7 +366,7 @@ cudaError_t launch_expert_combine(const uint16_t* Y, int64_t T, int64_t N, int64
                                   cudaStream_t stream) {
   if (M == 0) return cudaSuccess;
   const bool vec = N % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0;
-  const int64_t per = kCombineThreads * (vec ? 8 : 1);
+  const int64_t per = kCombineThreads * (vec ? 8 : 4);
   const unsigned int grid = static_cast<unsigned int>(M * ((N + per - 1) / per));
   return vec ? launch_pdl(expert_combine_kernel<true>, grid, kCombineThreads, 0, stream, Y, T, N, ldy, pos, weights, k,
                           out, ldo)

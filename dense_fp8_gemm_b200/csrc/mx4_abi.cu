@@ -442,7 +442,7 @@ size_t spense_expert_sort_workspace_size(int64_t M, int64_t k, int64_t E) {
     fail(SPENSE_ERR_SHAPE, "M = %lld, k = %lld or E = %lld out of range", (long long)M, (long long)k, (long long)E);
     return 0;
   }
-  return round_up(static_cast<size_t>(expert_sort_chunks(M * k) * E) * 4, 256);
+  return round_up(static_cast<size_t>(expert_sort_counts(M * k, E)) * 4, 256);
 }
 
 spense_status spense_expert_sort(const void* ids, int id_bits, int64_t M, int64_t k, int64_t E, int32_t* offsets,

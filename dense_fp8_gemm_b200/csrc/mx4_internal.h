@@ -77,7 +77,8 @@ cudaError_t launch_mx4_dequantize(const uint8_t* Xq, const uint8_t* xs, bool wor
 cudaError_t launch_mx4_pack(const uint8_t* Wq, const uint8_t* ws, int64_t E, int64_t N, int64_t K, int n_tiles,
                             int kblocks, uint8_t* blocks, unsigned int* err, cudaStream_t stream);
 
-int64_t expert_sort_chunks(int64_t n);
+// int32 counters expert_sort keeps in its workspace.
+int64_t expert_sort_counts(int64_t n, int64_t E);
 cudaError_t launch_expert_sort(const void* ids, bool wide, int64_t n, int k, int E, int32_t* offsets, int32_t* rows,
                                int32_t* pos, int32_t* counts, cudaStream_t stream);
 cudaError_t launch_expert_combine(const uint16_t* Y, int64_t T, int64_t N, int64_t ldy, const int32_t* pos,

@@ -23,46 +23,30 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight consecutive values as floats (exact for every input type).
-struct Raw8 {
-  uint4 a, b;
-};
-
-template <int kType>
-__device__ __forceinline__ Raw8 load8(const void* row, int64_t col) {
-  Raw8 r;
-  if constexpr (kType == SPENSE_TYPE_F32) {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + col);
-    r.a = __ldg(s);
-    r.b = __ldg(s + 1);
-  } else {
-    r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + col));
-    r.b = make_uint4(0u, 0u, 0u, 0u);
-  }
-  return r;
-}
-
-template <int kType>
-__device__ __forceinline__ void to_float8(const Raw8& r, float (&f)[8]) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+// kN 16-byte pieces of consecutive values as floats (exact for every input type).
+template <int kType, int kN>
+__device__ __forceinline__ void to_floats(const uint4 (&raw)[kN], float* f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kType == SPENSE_TYPE_F32) {
-      f[2 * i] = __uint_as_float(w[2 * i]);
-      f[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
-    } else if constexpr (kType == SPENSE_TYPE_BF16) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    } else {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
+  for (int i = 0; i < kN; ++i) {
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kType == SPENSE_TYPE_F32) {
+        f[4 * i + j] = __uint_as_float(w[j]);
+      } else if constexpr (kType == SPENSE_TYPE_BF16) {
+        f[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        f[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        f[8 * i + 2 * j] = v.x;
+        f[8 * i + 2 * j + 1] = v.y;
+      }
     }
   }
 }
 
 // Eight floats -> eight e2m1 codes, the first in the low nibble.
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&f)[8]) {
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* f) {
   uint32_t r;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -75,88 +59,100 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&f)[8]) {
   return r;
 }
 
-// The work of both kernels: a warp covers 256 columns of a row at a time, eight
-// a lane, so a block of 32 columns is four lanes and a scale word (128 columns)
-// sixteen. kWide (many rows): the eight warps of a CTA take eight rows and each
-// four such pieces of its row, all loads issued first; the CTA's scale words of
-// one column group are eight consecutive words (one 32-byte sector). Otherwise
-// (few rows) the eight warps take eight pieces of one row, one load a lane, so
-// one token of 5120 columns spreads over three CTAs.
+// The work of both kernels. A thread takes 16 columns, two threads a block, eight a scale word
+// (128 columns), a warp 512 columns.
+//   kWide (many rows): the eight warps of a CTA take eight rows and each two such
+//     pieces of its row, all loads first. The CTA's scale words leave through
+//     shared memory, eight rows' words of a column group (32 bytes) at a time:
+//     written one by one they were twice as many requests as the codes (32768
+//     gathered rows of 5120 with eight columns a thread: 90 us; now 64).
+//   else (few rows): the eight warps take eight pieces of one row, so a token's
+//     5120 columns are two CTAs with one round of loads.
 template <bool kWide>
-struct Where {
-  static constexpr int kPieces = kWide ? 4 : 1;
-  static constexpr int kRowsPerCta = kWide ? 8 : 1;
-  static constexpr int kColsPerCta = kWide ? 1024 : 2048;
-  int64_t row;
-  int64_t col0;  // this lane's first column of piece 0; piece i is 256 columns on
-  __device__ Where(int64_t K) {
-    const int64_t spans = (K + kColsPerCta - 1) / kColsPerCta;
-    const int64_t rb = blockIdx.x / spans, sb = blockIdx.x - rb * spans;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    row = rb * kRowsPerCta + (kWide ? warp : 0);
-    col0 = sb * kColsPerCta + (kWide ? 0 : warp * 256) + lane * 8;
+struct RowTile {
+  static constexpr int kPieces = kWide ? 2 : 1;
+  static constexpr int kRows = kWide ? 8 : 1;
+  static constexpr int kCols = kWide ? 1024 : 4096;
+  static unsigned int grid(int64_t T, int64_t K) {
+    return static_cast<unsigned int>(((T + kRows - 1) / kRows) * ((K + kCols - 1) / kCols));
   }
 };
 
-template <bool kWide>
-unsigned int where_grid(int64_t T, int64_t K) {
-  using W = Where<kWide>;
-  return static_cast<unsigned int>(((T + W::kRowsPerCta - 1) / W::kRowsPerCta) *
-                                   ((K + W::kColsPerCta - 1) / W::kColsPerCta));
-}
-
 template <int kType, bool kWide>
 __global__ void __launch_bounds__(kThreads)
-    mx4_quantize_kernel(const void* __restrict__ X, int64_t T, int64_t K, int64_t ldx,
-                        const int32_t* __restrict__ rows, int64_t M_src, uint8_t* __restrict__ Xq,
-                        uint8_t* __restrict__ xs, int words) {
-  using W = Where<kWide>;
+    mx4_quantize_kernel(const void* __restrict__ X, int T, int K, int64_t ldx, const int32_t* __restrict__ rows,
+                        int M_src, uint8_t* __restrict__ Xq, uint8_t* __restrict__ xs, int words) {
+  using Q = RowTile<kWide>;
+  constexpr int kSize = kType == SPENSE_TYPE_F32 ? 4 : 2;
+  constexpr int kLoads = kSize;  // 16-byte loads for 16 values
+  __shared__ uint32_t staged[kWide ? 64 : 1];  // [column group][row]
+  __shared__ int live_row[kWide ? 8 : 1];
   pdl_trigger();
-  const W w(K);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned int spans = static_cast<unsigned int>((K + Q::kCols - 1) / Q::kCols);
+  const unsigned int rb = blockIdx.x / spans;
+  const int span0 = static_cast<int>(blockIdx.x - rb * spans) * Q::kCols;
+  const int row0 = static_cast<int>(rb) * Q::kRows;
+  const int row = row0 + (kWide ? warp : 0);
+  const int col0 = span0 + (kWide ? 0 : warp * 512) + lane * 16;
   pdl_wait();
-  if (w.row >= T) return;
-  int64_t src = w.row;
-  if (rows != nullptr) {
-    src = __ldg(rows + w.row);
-    if (src < 0 || src >= M_src) return;  // the whole warp: the row is left as it was
+  int src = -1;  // the warp's source row, or none
+  if (row < T) {
+    src = rows != nullptr ? __ldg(rows + row) : row;
+    if (src >= M_src) src = -1;
   }
-  const int64_t esize = kType == SPENSE_TYPE_F32 ? 4 : 2;
-  const void* xrow = static_cast<const uint8_t*>(X) + src * ldx * esize;
-  Raw8 raw[W::kPieces];
+  const char* xrow = static_cast<const char*>(X) + static_cast<int64_t>(src) * ldx * kSize;
+  uint4 raw[Q::kPieces][kLoads];
 #pragma unroll
-  for (int i = 0; i < W::kPieces; ++i) {
-    const int64_t c = w.col0 + 256 * i;
-    raw[i].a = raw[i].b = make_uint4(0u, 0u, 0u, 0u);
-    if (c < K) raw[i] = load8<kType>(xrow, c);
+  for (int i = 0; i < Q::kPieces; ++i) {
+    const int c = col0 + 512 * i;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      raw[i][j] = make_uint4(0u, 0u, 0u, 0u);
+      if (src >= 0 && c < K) raw[i][j] = __ldg(reinterpret_cast<const uint4*>(xrow + c * kSize) + j);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < W::kPieces; ++i) {
-    const int64_t c = w.col0 + 256 * i;
-    float f[8];
-    to_float8<kType>(raw[i], f);
+  for (int i = 0; i < Q::kPieces; ++i) {
+    const int c = col0 + 512 * i;
+    float f[16];
+    to_floats<kType, kLoads>(raw[i], f);
     // Magnitudes as bit patterns: ordered like the values, infinities and NaN above all.
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     // Scale byte e + 127 = (biased exponent of the largest magnitude) - 2, from
     // below cut at 0 (zeros, subnormals); 255 marks a block that is not finite.
     const uint32_t ex = m >> 23;
     const uint32_t byte = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
     const float inv = __uint_as_float(byte == 255u ? 0x3F800000u : (254u - byte) << 23);  // 2^-e
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= inv;
-    const uint32_t codes = cvt_e2m1x8(f);
-    if (c < K) *reinterpret_cast<uint32_t*>(Xq + w.row * (K / 2) + c / 2) = codes;
+    for (int j = 0; j < 16; ++j) f[j] *= inv;
+    const bool live = src >= 0 && c < K;
+    if (live)
+      *reinterpret_cast<uint2*>(Xq + (static_cast<int64_t>(row) * K + c) / 2) =
+          make_uint2(cvt_e2m1x8(f), cvt_e2m1x8(f + 8));
     if (words) {
-      uint32_t v = c < K ? byte << (8 * ((lane >> 2) & 3)) : 0u;  // bytes past K are 0
+      uint32_t v = c < K ? byte << (8 * ((lane >> 1) & 3)) : 0u;  // bytes past K are 0
+      v |= __shfl_xor_sync(0xffffffffu, v, 2);
       v |= __shfl_xor_sync(0xffffffffu, v, 4);
-      v |= __shfl_xor_sync(0xffffffffu, v, 8);
-      if ((lane & 15) == 0 && c < K) reinterpret_cast<uint32_t*>(xs)[(c / 128) * T + w.row] = v;
-    } else if ((lane & 3) == 0 && c < K) {
-      xs[w.row * (K / 32) + c / 32] = static_cast<uint8_t>(byte);
+      if constexpr (kWide) {
+        if ((lane & 7) == 0) staged[(4 * i + (lane >> 3)) * 8 + warp] = v;
+      } else {
+        if ((lane & 7) == 0 && live) reinterpret_cast<uint32_t*>(xs)[static_cast<int64_t>(c / 128) * T + row] = v;
+      }
+    } else if ((lane & 1) == 0 && live) {
+      xs[static_cast<int64_t>(row) * (K / 32) + c / 32] = static_cast<uint8_t>(byte);
+    }
+  }
+  if constexpr (kWide) {
+    if (words) {  // the same for the whole grid
+      if (lane == 0) live_row[warp] = src >= 0;
+      __syncthreads();
+      const int t = threadIdx.x, g = span0 / 128 + (t >> 3), r = t & 7;
+      if (t < 64 && g * 128 < K && live_row[r])
+        reinterpret_cast<uint32_t*>(xs)[static_cast<int64_t>(g) * T + row0 + r] = staged[t];
     }
   }
 }
@@ -179,49 +175,80 @@ __device__ __forceinline__ void e2m1x8_to_float(uint32_t codes, float (&f)[8]) {
   }
 }
 
+// 32-byte store (address 32-byte aligned).
+__device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Dequantiser. A thread takes 16 columns (half a block: one scale, 32 bytes of bf16
+// output in one store when the output is 32-byte aligned), a warp 512 columns of a
+// row; kWide: eight rows a CTA, two pieces a warp, all loads first; else eight
+// pieces of one row.
+//
 // Every value is exact in the output type (three significant bits; 2^-128 at
 // least) up to 6 x 2^125; larger ones, which the quantiser never makes, may
 // round to infinity.
 template <bool kF32, bool kWide>
 __global__ void __launch_bounds__(kThreads)
-    mx4_dequantize_kernel(const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ xs, int words, int64_t T,
-                          int64_t K, void* __restrict__ Y) {
-  using W = Where<kWide>;
+    mx4_dequantize_kernel(const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ xs, int words, int T, int K,
+                          void* __restrict__ Y) {
+  using Q = RowTile<kWide>;
   pdl_trigger();
-  const W w(K);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned int spans = static_cast<unsigned int>((K + Q::kCols - 1) / Q::kCols);
+  const unsigned int rb = blockIdx.x / spans;
+  const int row = static_cast<int>(rb) * Q::kRows + (kWide ? warp : 0);
+  const int col0 = static_cast<int>(blockIdx.x - rb * spans) * Q::kCols + (kWide ? 0 : warp * 512) + lane * 16;
   pdl_wait();
-  if (w.row >= T) return;
-  uint32_t codes[W::kPieces], byte[W::kPieces];
+  if (row >= T) return;
+  uint2 codes[Q::kPieces];
+  uint32_t byte[Q::kPieces];
 #pragma unroll
-  for (int i = 0; i < W::kPieces; ++i) {
-    const int64_t c = w.col0 + 256 * i;
-    codes[i] = byte[i] = 0u;
+  for (int i = 0; i < Q::kPieces; ++i) {
+    const int c = col0 + 512 * i;
+    codes[i] = make_uint2(0u, 0u);
+    byte[i] = 0u;
     if (c < K) {
-      codes[i] = __ldg(reinterpret_cast<const uint32_t*>(Xq + w.row * (K / 2) + c / 2));
-      byte[i] = words ? __ldg(xs + ((c / 128) * T + w.row) * 4 + (c / 32) % 4) : __ldg(xs + w.row * (K / 32) + c / 32);
+      codes[i] = __ldg(reinterpret_cast<const uint2*>(Xq + (static_cast<int64_t>(row) * K + c) / 2));
+      byte[i] = words ? __ldg(xs + (static_cast<int64_t>(c / 128) * T + row) * 4 + (c / 32) % 4)
+                      : __ldg(xs + static_cast<int64_t>(row) * (K / 32) + c / 32);
     }
   }
 #pragma unroll
-  for (int i = 0; i < W::kPieces; ++i) {
-    const int64_t c = w.col0 + 256 * i;
+  for (int i = 0; i < Q::kPieces; ++i) {
+    const int c = col0 + 512 * i;
     if (c >= K) break;
-    float f[8];
-    e2m1x8_to_float(codes[i], f);
     const float s = scale_value(byte[i]);
+    const int64_t at = static_cast<int64_t>(row) * K + c;
+    uint32_t o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= s;
-    if constexpr (kF32) {
-      float4* y = reinterpret_cast<float4*>(static_cast<float*>(Y) + w.row * K + c);
-      y[0] = make_float4(f[0], f[1], f[2], f[3]);
-      y[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-      uint32_t o[4];
+    for (int h = 0; h < 2; ++h) {
+      float f[8];
+      e2m1x8_to_float(h == 0 ? codes[i].x : codes[i].y, f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-        o[j] = *reinterpret_cast<const uint32_t*>(&v);
+      for (int j = 0; j < 8; ++j) f[j] *= s;
+      if constexpr (kF32) {
+        float4* y = reinterpret_cast<float4*>(static_cast<float*>(Y) + at + 8 * h);
+        y[0] = make_float4(f[0], f[1], f[2], f[3]);
+        y[1] = make_float4(f[4], f[5], f[6], f[7]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+          o[4 * h + j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
       }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(Y) + w.row * K + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if constexpr (!kF32) {
+      uint16_t* y = static_cast<uint16_t*>(Y) + at;
+      if ((reinterpret_cast<uintptr_t>(Y) & 31) == 0) {
+        st_global_v8(y, o);
+      } else {
+        reinterpret_cast<uint4*>(y)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4*>(y)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
   }
 }
@@ -262,42 +289,44 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int kType>
 cudaError_t quantize_typed(const void* X, int64_t T, int64_t K, int64_t ldx, const int32_t* rows, int64_t M_src,
-                           uint8_t* Xq, uint8_t* xs, bool words, bool wide, cudaStream_t stream) {
-  return wide ? launch_pdl(mx4_quantize_kernel<kType, true>, where_grid<true>(T, K), kThreads, 0, stream, X, T, K, ldx,
-                           rows, M_src, Xq, xs, static_cast<int>(words))
-              : launch_pdl(mx4_quantize_kernel<kType, false>, where_grid<false>(T, K), kThreads, 0, stream, X, T, K,
-                           ldx, rows, M_src, Xq, xs, static_cast<int>(words));
+                           uint8_t* Xq, uint8_t* xs, bool words, int sms, cudaStream_t stream) {
+  const int t = static_cast<int>(T), k = static_cast<int>(K), m = static_cast<int>(M_src), w = words ? 1 : 0;
+  // Eight rows a CTA once that fills the device twice over.
+  if (RowTile<true>::grid(T, K) >= 2u * static_cast<unsigned int>(sms))
+    return launch_pdl(mx4_quantize_kernel<kType, true>, RowTile<true>::grid(T, K), kThreads, 0, stream, X, t, k, ldx,
+                      rows, m, Xq, xs, w);
+  return launch_pdl(mx4_quantize_kernel<kType, false>, RowTile<false>::grid(T, K), kThreads, 0, stream, X, t, k, ldx,
+                    rows, m, Xq, xs, w);
 }
 
-// Eight rows a CTA once that fills the device twice over.
-bool wide_rows(int64_t T, int64_t K, int sms) { return where_grid<true>(T, K) >= 2u * static_cast<unsigned int>(sms); }
+template <bool kF32>
+cudaError_t dequantize_typed(const uint8_t* Xq, const uint8_t* xs, bool words, int64_t T, int64_t K, void* Y, int sms,
+                             cudaStream_t stream) {
+  const int t = static_cast<int>(T), k = static_cast<int>(K), w = words ? 1 : 0;
+  if (RowTile<true>::grid(T, K) >= 2u * static_cast<unsigned int>(sms))
+    return launch_pdl(mx4_dequantize_kernel<kF32, true>, RowTile<true>::grid(T, K), kThreads, 0, stream, Xq, xs, w,
+                      t, k, Y);
+  return launch_pdl(mx4_dequantize_kernel<kF32, false>, RowTile<false>::grid(T, K), kThreads, 0, stream, Xq, xs, w,
+                    t, k, Y);
+}
 
 }  // namespace
 
 cudaError_t launch_mx4_quantize(const void* X, int x_type, int64_t T, int64_t K, int64_t ldx, const int32_t* rows,
                                 int64_t M_src, uint8_t* Xq, uint8_t* xs, bool words, int sms, cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
-  const bool wide = wide_rows(T, K, sms);
   if (x_type == SPENSE_TYPE_F32)
-    return quantize_typed<SPENSE_TYPE_F32>(X, T, K, ldx, rows, M_src, Xq, xs, words, wide, stream);
+    return quantize_typed<SPENSE_TYPE_F32>(X, T, K, ldx, rows, M_src, Xq, xs, words, sms, stream);
   if (x_type == SPENSE_TYPE_F16)
-    return quantize_typed<SPENSE_TYPE_F16>(X, T, K, ldx, rows, M_src, Xq, xs, words, wide, stream);
-  return quantize_typed<SPENSE_TYPE_BF16>(X, T, K, ldx, rows, M_src, Xq, xs, words, wide, stream);
+    return quantize_typed<SPENSE_TYPE_F16>(X, T, K, ldx, rows, M_src, Xq, xs, words, sms, stream);
+  return quantize_typed<SPENSE_TYPE_BF16>(X, T, K, ldx, rows, M_src, Xq, xs, words, sms, stream);
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t* Xq, const uint8_t* xs, bool words, int64_t T, int64_t K, void* Y,
                                   int y_type, int sms, cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
-  const bool wide = wide_rows(T, K, sms);
-  const bool f32 = y_type == SPENSE_TYPE_F32;
-  auto go = [&](auto kernel, unsigned int grid) {
-    return launch_pdl(kernel, grid, kThreads, 0, stream, Xq, xs, static_cast<int>(words), T, K, Y);
-  };
-  if (f32)
-    return wide ? go(mx4_dequantize_kernel<true, true>, where_grid<true>(T, K))
-                : go(mx4_dequantize_kernel<true, false>, where_grid<false>(T, K));
-  return wide ? go(mx4_dequantize_kernel<false, true>, where_grid<true>(T, K))
-              : go(mx4_dequantize_kernel<false, false>, where_grid<false>(T, K));
+  return y_type == SPENSE_TYPE_F32 ? dequantize_typed<true>(Xq, xs, words, T, K, Y, sms, stream)
+                                   : dequantize_typed<false>(Xq, xs, words, T, K, Y, sms, stream);
 }
 
 cudaError_t launch_mx4_pack(const uint8_t* Wq, const uint8_t* ws, int64_t E, int64_t N, int64_t K, int n_tiles,

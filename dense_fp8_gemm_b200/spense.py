@@ -8,6 +8,7 @@ PyTorch supplies device memory and streams; tensors are passed by address.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -565,27 +566,38 @@ def select_dense(score: torch.Tensor, Kd: int, out: torch.Tensor | None = None, 
     return out
 
 
-def _current(name: str, *tensors):
-    """The device of `tensors`, which has to be the current one: the library
-    launches there, and addresses of another device mean nothing on it."""
-    dev = _device_index()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{dev}")
+def _addr(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of that type on the current device, `dev`
+    (where the library launches: another device's addresses mean nothing there)."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _row_strided(t: torch.Tensor, name: str):
-    """Address and row stride of a 2-D CUDA tensor with unit column stride (a
+def _rows_addr(t: torch.Tensor, dtype, dev: int, name: str, rows: int, cols: int):
+    """Address and row stride of a [rows, cols] tensor with unit column stride (a
     column slice of a wider one may be given; rows may not overlap)."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
-    ld = t.stride(0) if rows > 1 else cols
-    if ld < cols:
-        raise ValueError(f"{name} must have rows that do not overlap")
+    if t.is_contiguous():
+        ld = cols
+    else:
+        ld = t.stride(0) if rows > 1 else cols
+        if (cols > 1 and t.stride(1) != 1) or ld < cols:
+            raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device, cuda:{dev}; it is on {t.device}")
     return t.data_ptr(), ld
+
+
+def _raw(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _scale_flags(x_scale: torch.Tensor, M: int, K: int) -> int:
@@ -605,27 +617,28 @@ def mx4_quantize(X: torch.Tensor, rows: torch.Tensor | None = None, scale_rows: 
     outside [0, M) leave their output row as it was). Returns (Xq uint8
     [T, K / 2], x_scale uint8): scales as words [ceil(K / 128), T, 4], or
     [T, K / 32] with scale_rows (the layout mx4_pack takes)."""
-    if X.dtype not in MX4_TYPES:
-        raise TypeError(f"X must be bfloat16, float16 or float32, got {X.dtype}")
-    ptr, ldx = _row_strided(X, "X")
+    dtype = X.dtype
+    if dtype not in MX4_TYPES:
+        raise TypeError(f"X must be bfloat16, float16 or float32, got {dtype}")
+    if X.dim() != 2 or (rows is not None and rows.dim() != 1):
+        raise ValueError("X must be 2-D and rows 1-D")
+    dev = _device_index()
     M, K = X.shape
-    T = M if rows is None else rows.shape[0]
+    x, ldx = _rows_addr(X, dtype, dev, "X", M, K)
+    T, r = (M, None) if rows is None else (rows.shape[0], _addr(rows, torch.int32, dev, "rows"))
     if Xq is None:
         Xq = torch.empty((T, K // 2), dtype=torch.uint8, device=X.device)
+    elif Xq.shape != (T, K // 2):
+        raise ValueError(f"Xq must be [{T}, {K // 2}], got {tuple(Xq.shape)}")
     if x_scale is None:
         x_scale = torch.empty((T, K // 32) if scale_rows else (-(-K // 128), T, 4), dtype=torch.uint8, device=X.device)
-    if Xq.shape != (T, K // 2):
-        raise ValueError(f"Xq must be [{T}, {K // 2}], got {tuple(Xq.shape)}")
-    if rows is not None and rows.dim() != 1:
-        raise ValueError("rows must be 1-D")
-    flags = MX4_SCALE_ROWS if scale_rows else _scale_flags(x_scale, T, K)
-    if scale_rows and x_scale.shape != (T, K // 32):
+    elif scale_rows and x_scale.shape != (T, K // 32):
         raise ValueError(f"x_scale must be [{T}, {K // 32}], got {tuple(x_scale.shape)}")
-    _current("mx4_quantize", X, rows, Xq, x_scale)
-    code = lib().spense_mx4_quantize(ptr, MX4_TYPES[X.dtype], M, K, ldx, _dev_ptr(rows, torch.int32, "rows"), T,
-                                     _dev_ptr(Xq, torch.uint8, "Xq"), _dev_ptr(x_scale, torch.uint8, "x_scale"),
-                                     flags, _stream(stream))
-    _check(code, "spense_mx4_quantize")
+    flags = MX4_SCALE_ROWS if scale_rows else _scale_flags(x_scale, T, K)
+    code = lib().spense_mx4_quantize(x, MX4_TYPES[dtype], M, K, ldx, r, T, _addr(Xq, torch.uint8, dev, "Xq"),
+                                     _addr(x_scale, torch.uint8, dev, "x_scale"), flags, _raw(stream, dev))
+    if code != SPENSE_OK:
+        _check(code, "spense_mx4_quantize")
     return Xq, x_scale
 
 
@@ -633,17 +646,20 @@ def mx4_dequantize(Xq: torch.Tensor, x_scale: torch.Tensor, dtype=torch.bfloat16
                    stream=None) -> torch.Tensor:
     """spense_mx4_dequantize: the values [M, K] of codes [M, K / 2] and their scales
     (either layout), as bfloat16 or float32."""
-    M, K = Xq.shape[0], Xq.shape[1] * 2
+    if Xq.dim() != 2:
+        raise ValueError("Xq must be 2-D")
+    dev = _device_index()
+    M, K = Xq.shape
+    K *= 2
     if out is None:
         out = torch.empty((M, K), dtype=dtype, device=Xq.device)
     if out.shape != (M, K) or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"the output must be bfloat16 or float32 [{M}, {K}], got {out.dtype} {tuple(out.shape)}")
-    flags = _scale_flags(x_scale, M, K)
-    _current("mx4_dequantize", Xq, x_scale, out)
-    code = lib().spense_mx4_dequantize(_dev_ptr(Xq, torch.uint8, "Xq"), _dev_ptr(x_scale, torch.uint8, "x_scale"), M,
-                                       K, _dev_ptr(out, out.dtype, "out"), MX4_TYPES[out.dtype], flags,
-                                       _stream(stream))
-    _check(code, "spense_mx4_dequantize")
+    code = lib().spense_mx4_dequantize(_addr(Xq, torch.uint8, dev, "Xq"), _addr(x_scale, torch.uint8, dev, "x_scale"),
+                                       M, K, _addr(out, out.dtype, dev, "out"), MX4_TYPES[out.dtype],
+                                       _scale_flags(x_scale, M, K), _raw(stream, dev))
+    if code != SPENSE_OK:
+        _check(code, "spense_mx4_dequantize")
     return out
 
 
@@ -698,11 +714,11 @@ def mx4_pack(Wq: torch.Tensor, w_scale: torch.Tensor, stream=None) -> Mx4Weight:
     if Wq.dim() not in (2, 3) or w_scale.shape != (*Wq.shape[:-1], Wq.shape[-1] // 16):
         raise ValueError(f"codes [.., N, K / 2] and scales [.., N, K / 32] expected, got {tuple(Wq.shape)} and "
                          f"{tuple(w_scale.shape)}")
+    dev = _device_index()
     E, (N, K) = (Wq.shape[0] if Wq.dim() == 3 else 1), (Wq.shape[-2], Wq.shape[-1] * 2)
-    _current("mx4_pack", Wq, w_scale)
     out = ctypes.c_void_p()
-    code = lib().spense_mx4_pack(_dev_ptr(Wq, torch.uint8, "Wq"), _dev_ptr(w_scale, torch.uint8, "w_scale"), E, N, K,
-                                 _stream(stream), ctypes.byref(out))
+    code = lib().spense_mx4_pack(_addr(Wq, torch.uint8, dev, "Wq"), _addr(w_scale, torch.uint8, dev, "w_scale"), E, N,
+                                 K, _raw(stream, dev), ctypes.byref(out))
     _check(code, "spense_mx4_pack")
     return Mx4Weight(out)
 
@@ -730,19 +746,21 @@ class PreparedMx4Gemm:
             raise ValueError(f"Y must be bfloat16 [{M}, {pw.N}], got {Y.dtype} {tuple(Y.shape)}")
         if offsets is not None and offsets.shape != (pw.E + 1,):
             raise ValueError(f"offsets must be [{pw.E + 1}], got {tuple(offsets.shape)}")
-        _current("mx4_gemm", Xq, x_scale, Y, workspace, offsets)
-        y, ldy = _row_strided(Y, "Y")
+        dev = self._dev = _device_index()
+        y, ldy = _rows_addr(Y, torch.bfloat16, dev, "Y", M, pw.N)
         self._keep = (pw, Xq, x_scale, Y, workspace, offsets)
         self._where = "spense_mx4_gemm" if offsets is None else "spense_mx4_gemm_experts"
         self._fn = getattr(lib(), self._where)
-        args = [pw.handle, _dev_ptr(Xq, torch.uint8, "Xq"), _dev_ptr(x_scale, torch.uint8, "x_scale"), M]
+        args = [pw.handle, _addr(Xq, torch.uint8, dev, "Xq"), _addr(x_scale, torch.uint8, dev, "x_scale"), M]
         if offsets is not None:
-            args.append(_dev_ptr(offsets, torch.int32, "offsets"))
-        self._args = (*args, ctypes.c_void_p(y), max(ldy, pw.N), _dev_ptr(workspace, torch.uint8, "workspace"),
-                      workspace.numel())
+            args.append(_addr(offsets, torch.int32, dev, "offsets"))
+        args += [y, ldy, _addr(workspace, torch.uint8, dev, "workspace"), workspace.numel()]
+        self._args = tuple(ctype(a) if not isinstance(a, ctypes.c_void_p) else a
+                           for ctype, a in zip(self._fn.argtypes, args))
 
     def __call__(self, stream=None):
-        code = self._fn(*self._args, _stream(stream))
+        """On the device of the tensors, which has to be the current one."""
+        code = self._fn(*self._args, _raw(stream, self._dev))
         if code != SPENSE_OK:
             _check(code, self._where)
 
@@ -772,35 +790,42 @@ def mx4_gemm_experts(pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, off
     return Y
 
 
+@functools.lru_cache(maxsize=256)
+def _sort_workspace(M: int, k: int, E: int) -> int:
+    return int(lib().spense_expert_sort_workspace_size(M, k, E))
+
+
 def expert_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None,
                 pos: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """spense_expert_sort: choices ids [M, k] (int32 or int64; outside [0, E): left
     out) sorted by expert, stably. Returns (offsets int32 [E + 1], rows int32
     [M k]: the token of every slot, -1 behind the last; pos int32 [M, k]: the slot
-    of every choice, -1 for one left out)."""
-    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
-        raise ValueError(f"ids must be int32 or int64 [M, k], got {ids.dtype} {tuple(ids.shape)}")
+    of every choice, -1 for one left out). What is not given is made here, in one
+    allocation."""
+    dtype = ids.dtype
+    if ids.dim() != 2 or dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64 [M, k], got {dtype} {tuple(ids.shape)}")
+    dev = _device_index()
     M, k = ids.shape
-    dev = ids.device
-    if offsets is None:
-        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
-    if rows is None:
-        rows = torch.empty((M * k,), dtype=torch.int32, device=dev)
-    if pos is None:
-        pos = torch.empty((M, k), dtype=torch.int32, device=dev)
-    if offsets.shape != (E + 1,) or rows.shape != (M * k,) or pos.shape != (M, k):
-        raise ValueError(f"offsets [{E + 1}], rows [{M * k}] and pos [{M}, {k}] expected")
-    if workspace is None:
-        need = int(lib().spense_expert_sort_workspace_size(M, k, E))
+    n = M * k
+    if offsets is None or rows is None or pos is None or workspace is None:
+        need = _sort_workspace(M, k, E) // 4
         if need == 0:
             _check(2, "spense_expert_sort")
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    _current("expert_sort", ids, offsets, rows, pos, workspace)
-    code = lib().spense_expert_sort(_dev_ptr(ids, ids.dtype, "ids"), 32 if ids.dtype == torch.int32 else 64, M, k, E,
-                                    _dev_ptr(offsets, torch.int32, "offsets"), _dev_ptr(rows, torch.int32, "rows"),
-                                    _dev_ptr(pos, torch.int32, "pos"), _dev_ptr(workspace, torch.uint8, "workspace"),
-                                    workspace.numel(), _stream(stream))
-    _check(code, "spense_expert_sort")
+        ws, r, p, o = torch.empty(need + 2 * n + E + 1, dtype=torch.int32, device=ids.device).split((need, n, n, E + 1))
+        workspace = ws if workspace is None else workspace
+        rows = r if rows is None else rows
+        pos = p.view(M, k) if pos is None else pos
+        offsets = o if offsets is None else offsets
+    if offsets.shape != (E + 1,) or rows.shape != (n,) or pos.shape != (M, k):
+        raise ValueError(f"offsets [{E + 1}], rows [{n}] and pos [{M}, {k}] expected")
+    code = lib().spense_expert_sort(_addr(ids, dtype, dev, "ids"), 32 if dtype is torch.int32 else 64, M, k, E,
+                                    _addr(offsets, torch.int32, dev, "offsets"), _addr(rows, torch.int32, dev, "rows"),
+                                    _addr(pos, torch.int32, dev, "pos"),
+                                    _addr(workspace, workspace.dtype, dev, "workspace"),
+                                    workspace.numel() * workspace.element_size(), _raw(stream, dev))
+    if code != SPENSE_OK:
+        _check(code, "spense_expert_sort")
     return offsets, rows, pos
 
 
@@ -809,20 +834,20 @@ def expert_combine(Y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, ou
     """spense_expert_combine: out[m] = sum_j weights[m, j] Y[pos[m, j]] in fp32, rounded
     to bf16; choices with pos outside Y's rows are left out. Y and out may be
     column slices of wider tensors."""
-    if Y.dtype != torch.bfloat16:
-        raise TypeError(f"Y must be bfloat16, got {Y.dtype}")
-    y, ldy = _row_strided(Y, "Y")
+    if Y.dim() != 2 or pos.dim() != 2 or weights.shape != pos.shape:
+        raise ValueError(f"Y [T, N], pos and weights [M, k] expected, got {tuple(Y.shape)}, {tuple(pos.shape)} and "
+                         f"{tuple(weights.shape)}")
+    dev = _device_index()
     T, N = Y.shape
-    if pos.dim() != 2 or weights.shape != pos.shape:
-        raise ValueError(f"pos and weights must be [M, k], got {tuple(pos.shape)} and {tuple(weights.shape)}")
     M, k = pos.shape
+    y, ldy = _rows_addr(Y, torch.bfloat16, dev, "Y", T, N)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=Y.device)
-    if out.shape != (M, N) or out.dtype != torch.bfloat16:
-        raise ValueError(f"out must be bfloat16 [{M}, {N}], got {out.dtype} {tuple(out.shape)}")
-    o, ldo = _row_strided(out, "out")
-    _current("expert_combine", Y, pos, weights, out)
-    code = lib().spense_expert_combine(y, T, N, ldy, _dev_ptr(pos, torch.int32, "pos"),
-                                       _dev_ptr(weights, torch.float32, "weights"), M, k, o, ldo, _stream(stream))
-    _check(code, "spense_expert_combine")
+    elif out.shape != (M, N):
+        raise ValueError(f"out must be [{M}, {N}], got {tuple(out.shape)}")
+    o, ldo = _rows_addr(out, torch.bfloat16, dev, "out", M, N)
+    code = lib().spense_expert_combine(y, T, N, ldy, _addr(pos, torch.int32, dev, "pos"),
+                                       _addr(weights, torch.float32, dev, "weights"), M, k, o, ldo, _raw(stream, dev))
+    if code != SPENSE_OK:
+        _check(code, "spense_expert_combine")
     return out
