@@ -69,20 +69,23 @@ double mx4_cost(int n, int split, int cps, int64_t tiles, int kblocks, double we
 // Few tiles: clusters of up to 8 CTAs split K, when the device holds all of them
 // at once and their partials fit the ring.
 //
-// Pairs (256 weight rows and up to 224 activation rows by two SMs) read a third
-// fewer bytes from L2 for the same products; they pay from 3e11 flops on, where
-// that outweighs the launch that orders their scales: 51200x5120 at 512, 1024 and
-// 8192 rows 74 -> 72, 128 -> 114 and 965 -> 845 us, but 10240x5120 at 2048 rows
-// 53 -> 56 us. Experts also need 128 rows on average, or a pair's tile is mostly
-// weights.
+// Pairs (256 weight rows and up to 192 activation rows by two SMs, as many as leave
+// tensor memory for two accumulators and five stages' scales) read a third fewer
+// bytes from L2 for the same products, but a launch in front orders their scales
+// and both CTAs fill before the first product. They pay from 4e11 flops on: 51200x5120
+// at 1024, 2048 and 4096 rows 126 -> 126, 272 -> 223 and 535 -> 425 us, 5120x27648 at
+// 2048 rows 129 -> 119 us, 10240x5120 at 2048 rows 57 -> 59 us. Experts also need 512
+// rows on average (8 x 5120x5120 at 2048 rows each 209 -> 188 us, 128 x 2560x2048 at
+// 256 rows each 132 -> 144 us) and all of them ten blocks of K (16 x 4096x1408: 145 ->
+// 158 us).
 spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, Mx4GemmPlan* out) {
   Mx4GemmPlan pl{};
   const uint32_t tail = static_cast<uint32_t>(round_up(kMx4BarrierBytes + 4 * (3 * static_cast<size_t>(E) + 1), 16));
   const int64_t active = ragged ? std::min(E, T) : 1;
   const double flops = 2.0 * T * n_tiles * kMx4Rows * kblocks * kMx4Cols;
   const int64_t avg = (T + E - 1) / E;
-  pl.pair = flops >= 3e11 && (ragged ? avg : T) >= 128 ? 1 : 0;
-  const int most = pl.pair ? 224 : kMx4MaxTile, step = pl.pair ? 32 : 16;
+  pl.pair = flops >= 4e11 && kblocks >= 10 && (!ragged || avg >= 512) ? 1 : 0;
+  const int most = pl.pair ? 192 : kMx4MaxTile, step = pl.pair ? 32 : 16;
   // Row tiles at most: every expert's last one may be short.
   auto row_tiles = [&](int n) { return ragged ? active + T / n : (T + n - 1) / n; };
   auto stage = [&](int n) {
@@ -100,7 +103,7 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
   for (int64_t m = m0; m < m0 + (ragged || pl.pair ? 1 : 16); ++m) {
     int n;
     if (ragged)
-      n = avg >= 112 ? 224 : static_cast<int>(std::min<int64_t>(round_up(std::max<int64_t>(2 * avg, 32), 16), 224));
+      n = pl.pair ? most : static_cast<int>(std::min<int64_t>(round_up(std::max<int64_t>(2 * avg, 32), 16), 208));
     else
       n = static_cast<int>(round_up((T + m - 1) / m, step));
     n = static_cast<int>(std::min<int64_t>(n, round_up(T, step)));
@@ -108,7 +111,7 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
     for (int s = 1; s <= (pl.pair ? 1 : 8); ++s) {
       const int cps = s > 1 && tiles * s > sms ? 2 : 1;
       if (s > 1) {
-        if (tiles * s > 2 * sms || kblocks < 2 * s || ring(n, cps) < 3 || n + 48 > 512 / cps) break;
+        if (tiles * s > 2 * sms || kblocks < 2 * s || ring(n, cps) < 3 || n + 72 > 512 / cps) break;
         const size_t partials = static_cast<size_t>(s - 1) * round_up((n + s - 1) / s, 8) * 512;
         if (partials > static_cast<size_t>(ring(n, cps)) * stage(n) || tiles > clusters_at_once(s, cps, sms)) continue;
       }
@@ -131,10 +134,14 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
   pl.stage_bytes = stage(pl.npad);
   pl.xs_bytes = slot(pl.npad);
   pl.stages = ring(pl.npad, pl.ctas_per_sm);
+  // Tensor memory: two accumulators where a CTA has several tiles, and 16 or 24
+  // scale columns a stage.
+  const int sf_cols = pl.npad > 128 ? 24 : 16, cols = 512 / pl.ctas_per_sm;
+  pl.nacc = pl.split == 1 && 2 * pl.npad + 4 * sf_cols <= cols ? 2 : 1;
+  pl.stages = std::min(pl.stages, (cols - pl.nacc * pl.npad) / sf_cols);
   if (pl.stages < 3) return fail(SPENSE_ERR_SHAPE, "no launch plan for %lld experts", (long long)E);
-  pl.nacc = pl.split == 1 && 2 * pl.npad + 48 <= 512 ? 2 : 1;
   pl.tmem_cols = 32;
-  while (pl.tmem_cols < static_cast<uint32_t>(pl.nacc * pl.npad + 48)) pl.tmem_cols <<= 1;
+  while (pl.tmem_cols < static_cast<uint32_t>(pl.nacc * pl.npad + pl.stages * sf_cols)) pl.tmem_cols <<= 1;
   pl.smem_bytes = 1024 + tail + kMx4XsSlots * pl.xs_bytes + static_cast<uint32_t>(pl.stages) * pl.stage_bytes;
   // A CTA that takes more than half of the tensor memory has the SM to itself.
   if (pl.tmem_cols > 256) pl.smem_bytes = std::max<uint32_t>(pl.smem_bytes, 122880u);

@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     Ring ring(static_cast<uint32_t>(p.stages)), xring(kXsSlots);
     const uint32_t sf_base = tmem_base + static_cast<uint32_t>(p.nacc * p.npad);
     const uint32_t atoms = (static_cast<uint32_t>(p.npad) + 127u) >> 7;
-    uint32_t sbuf = 0, acc = 0, aph = 1;
+    uint32_t acc = 0, aph = 1;
     bool ok = !(kPair && rank == 1);  // the even CTA issues the pair's MMAs
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
@@ -508,8 +508,10 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
           const uint64_t ad = ptx::desc_sw128(a_s), bd = ptx::desc_sw128(a_s + kMx4BlockBytes);
           const uint64_t wd = ptx::desc_rows16(a_s + kMx4CodeBytes), xd = ptx::desc_rows16(
               kPair ? a_s + kMx4BlockBytes + static_cast<uint32_t>(p.npad / 2) * 128u : xs_base + xring.s * p.xs_bytes);
-          // Scales: 8 columns for the weights' two column groups, then 8 a group for the activations.
-          const uint32_t sfa = sf_base + sbuf * 24u, sfb = sfa + 8u;
+          // Scales: 8 columns for the weights' two column groups, then 4 or 8 a group for
+          // the activations. Every stage has columns of its own, so that the stage's
+          // refill says that the products that read them have completed.
+          const uint32_t sfa = sf_base + ring.s * (8u + 8u * atoms), sfb = sfa + 8u;
           const uint32_t steps = kb + 1 == p.kblocks ? static_cast<uint32_t>(p.last_steps) : 4u;
           auto cp = [](uint32_t taddr, uint64_t desc) {
             if constexpr (kPair)
@@ -526,8 +528,8 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
 #pragma unroll
           for (uint32_t j = 0; j < 2; ++j) {
             cp(sfa + 4u * j, wd + 32u * j);
-            cp(sfb + 8u * j, xd + j * (group_bytes >> 4));
-            if (atoms > 1) cp(sfb + 8u * j + 4u, xd + j * (group_bytes >> 4) + 32u);
+            cp(sfb + 4u * atoms * j, xd + j * (group_bytes >> 4));
+            if (atoms > 1) cp(sfb + 4u * atoms * j + 4u, xd + j * (group_bytes >> 4) + 32u);
           }
           if constexpr (!kPair) commit(&bars->xs_empty[xring.s]);
 #pragma unroll
@@ -535,15 +537,14 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
             if (k >= steps) break;
             const uint32_t id = idesc ^ ((k & 1u) ? sf2 : 0u), accum = (kb > kb0 || k > 0) ? 1u : 0u;
             if constexpr (kPair)
-              ptx::mma_mxf4_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, sfa + 4u * (k >> 1), sfb + 8u * (k >> 1), accum);
+              ptx::mma_mxf4_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, sfa + 4u * (k >> 1), sfb + 4u * atoms * (k >> 1), accum);
             else
-              ptx::mma_mxf4(d_tmem, ad + 2u * k, bd + 2u * k, id, sfa + 4u * (k >> 1), sfb + 8u * (k >> 1), accum);
+              ptx::mma_mxf4(d_tmem, ad + 2u * k, bd + 2u * k, id, sfa + 4u * (k >> 1), sfb + 4u * atoms * (k >> 1), accum);
           }
           commit(&bars->empty[ring.s]);
           if (kb + 1 == kb1) commit(&bars->acc_full[acc]);
         }
         __syncwarp();
-        sbuf ^= 1u;
       }
       if (++acc == static_cast<uint32_t>(p.nacc)) {
         acc = 0;

@@ -282,3 +282,130 @@ def test_pack_rejects_nan_scales():
     with pytest.raises(spense.SpenseError) as e:
         spense.mx4_pack(q, s)
     assert e.value.code == 6
+
+
+def device_operands(seed, R, K):
+    """Codes and scale bytes drawn on the device (full sizes), scales over eight octaves."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randint(0, 256, (R, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.randint(121, 129, (R, K // 32), dtype=torch.uint8, device="cuda", generator=g)
+    return q, s
+
+
+def words_of(s):
+    return torch.nn.functional.pad(s, (0, -s.shape[1] % 4)).view(s.shape[0], -1, 4).permute(1, 0, 2).contiguous()
+
+
+def check_sampled(y, xq, xs, wq, ws, rows, seed):
+    """Sampled rows and columns of a large product (tile borders among them)."""
+    g = np.random.default_rng(seed)
+    N = wq.shape[0]
+    ms = np.unique(np.concatenate((rows[:1], rows[-1:], g.choice(rows, 24))))
+    ns = np.unique(np.concatenate(([0, 127, 128, 255, 256, N - 1], g.integers(0, N, 24), [N - 129, N - 128])))
+    x = ref.values(xq[ms].cpu().numpy(), xs[ms].cpu().numpy())
+    w = ref.values(wq[ns].cpu().numpy(), ws[ns].cpu().numpy())
+    want, tol = ref.gemm(x, w)
+    within(y[torch.from_numpy(ms).cuda()][:, torch.from_numpy(ns).cuda()], want, tol)
+
+
+@pytest.mark.parametrize("M,N,K", [(2053, 20001, 5152), (193, 160000, 6656), (4096, 19200, 2592)])
+def test_gemm_large_enough_for_pairs(M, N, K):
+    assert 2.0 * M * N * K >= 4e11                             # where the plan takes CTA pairs
+    wq, ws = device_operands(M, N, K)
+    xq, xs = device_operands(N, M, K)
+    pw = spense.mx4_pack(wq, ws)
+    wsp = spense.new_workspace(spense.mx4_workspace_size(pw, M))
+    assert wsp.numel() > 256
+    y = spense.mx4_gemm(pw, xq, words_of(xs), workspace=wsp)
+    again = spense.mx4_gemm(pw, xq, words_of(xs), workspace=wsp)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    assert spense.workspace_status(wsp) == 0
+    check_sampled(y, xq, xs, wq, ws, np.arange(M), M)
+    pw.free()
+
+
+@pytest.mark.parametrize("counts,spare", [([700, 0, 1500], 3), ([1, 2100, 31], 0)])
+def test_gemm_experts_large_enough_for_pairs(counts, spare):
+    E, T, N, K = len(counts), sum(counts) + spare, 20865, 4640
+    assert 2.0 * T * N * K >= 4e11 and T // E >= 512
+    wq, ws = device_operands(1, E * N, K)
+    xq, xs = device_operands(2, T, K)
+    pw = spense.mx4_pack(wq.view(E, N, -1), ws.view(E, N, -1))
+    off = offsets_of(counts)
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    wsp = spense.new_workspace(spense.mx4_workspace_size(pw, T))
+    spense.mx4_gemm_experts(pw, xq, words_of(xs), torch.from_numpy(off).cuda(), Y=y, workspace=wsp)
+    assert spense.workspace_status(wsp) == 0
+    for e in range(E):
+        if counts[e]:
+            check_sampled(y, xq, xs, wq[e * N:(e + 1) * N], ws[e * N:(e + 1) * N], np.arange(off[e], off[e + 1]), e)
+    assert bool((y[off[-1]:] == 7).all())
+    pw.free()
+
+
+def test_small_workspace_is_refused():
+    q, s, pw = packed(13, 1, 256, 512)
+    _, _, xqd, xsd = activations(14, 5, 512)
+    y = torch.empty((5, 256), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(spense.SpenseError) as e:
+        spense.mx4_gemm(pw, xqd, xsd, Y=y, workspace=spense.new_workspace(128))
+    assert e.value.code == 7
+    with pytest.raises(ValueError, match="words"):
+        spense.mx4_gemm(pw, xqd, torch.zeros((5, 16), dtype=torch.uint8, device="cuda"), Y=y)
+    many = spense.mx4_pack(torch.zeros((2, 8, 32), dtype=torch.uint8, device="cuda"),
+                           torch.full((2, 8, 2), 127, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(spense.SpenseError) as e:
+        spense.mx4_gemm(many, torch.zeros((1, 32), dtype=torch.uint8, device="cuda"),
+                        torch.zeros((1, 1, 4), dtype=torch.uint8, device="cuda"))
+    assert e.value.code == 1
+    with pytest.raises(ValueError, match="offsets"):
+        spense.mx4_gemm_experts(many, torch.zeros((1, 32), dtype=torch.uint8, device="cuda"),
+                                torch.zeros((1, 1, 4), dtype=torch.uint8, device="cuda"),
+                                torch.zeros(2, dtype=torch.int32, device="cuda"))
+    many.free()
+    pw.free()
+
+
+def test_two_streams_at_once():
+    """Products of two weights on two streams, each with its own workspace, many times over."""
+    K, sets = 2048, []
+    for i, (M, N) in enumerate(((3, 640), (130, 2560))):
+        q, s, pw = packed(20 + i, 1, N, K)
+        xq, xs, xqd, xsd = activations(30 + i, M, K)
+        y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        ws = spense.new_workspace(spense.mx4_workspace_size(pw, M))
+        want, tol = ref.gemm(ref.values(xq, xs), ref.values(q[0], s[0]))
+        sets.append((pw, xqd, xsd, y, ws, want, tol, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for pw, xqd, xsd, y, ws, _w, _t, stream in sets:
+            spense.mx4_gemm(pw, xqd, xsd, Y=y, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for pw, _x, _s, y, ws, want, tol, _st in sets:
+        within(y, want, tol)
+        assert spense.workspace_status(ws) == 0
+        pw.free()
+
+
+def test_beside_the_fp8_products_in_one_stream():
+    """MXFP4 and FP8 products in turn on one stream (each may start while the other ends)."""
+    from dense_fp8_gemm_b200 import synth
+    M, N, K = 16, 1024, 2048
+    W, s_w = synth.quantize_rows(synth.normal(3, 1, (N, K), 0.02))
+    X, s_x = synth.quantize_rows(synth.normal(3, 2, (M, K), 1.0))
+    p8 = spense.pack(torch.from_numpy(W).cuda(), torch.from_numpy(s_w).cuda(), Kd=K // 4)
+    x8, sx8 = torch.from_numpy(X).cuda(), torch.from_numpy(s_x).cuda()
+    w8 = spense.new_workspace(spense.workspace_size(p8, M))
+    q, s, p4 = packed(40, 1, N, K)
+    xq, xs, xqd, xsd = activations(41, M, K)
+    w4 = spense.new_workspace(spense.mx4_workspace_size(p4, M))
+    first = spense.gemm(p8, x8, sx8, workspace=w8).clone()
+    y8, y4 = torch.empty_like(first), torch.empty_like(first)
+    for _ in range(30):
+        spense.gemm(p8, x8, sx8, Y=y8, workspace=w8)
+        spense.mx4_gemm(p4, xqd, xsd, Y=y4, workspace=w4)
+    want, tol = ref.gemm(ref.values(xq, xs), ref.values(q[0], s[0]))
+    within(y4, want, tol)
+    assert torch.equal(y8.view(torch.int16), first.view(torch.int16))
+    p8.free()
+    p4.free()
