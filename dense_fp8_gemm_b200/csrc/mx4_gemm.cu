@@ -234,14 +234,15 @@ __device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y
   }
 }
 
-template <bool kPair>
+// kBlocks: blocks a stage holds.
+template <bool kPair, int kBlocks>
 __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     spense_mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const __grid_constant__ Mx4GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;  // the swizzled tiles are 1024-byte aligned
   const uint32_t xs_base = smem_base + static_cast<uint32_t>(p.stages) * p.stage_bytes;  // the scales' own ring
-  uint8_t* const tail = smem_raw + (xs_base - raw) + (kPair ? 0u : kXsSlots * p.xs_bytes);
+  uint8_t* const tail = smem_raw + (xs_base - raw) + (kPair ? 0u : kXsSlots / kBlocks * p.xs_bytes);
   Mx4Barriers* const bars = reinterpret_cast<Mx4Barriers*>(tail);
   TileList list;
   list.tile_begin = reinterpret_cast<int*>(tail + kMx4BarrierBytes);
@@ -322,6 +323,10 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
   // box and one tcgen05.cp, else a wide box and one or two.
   const uint32_t group_bytes = kPair || p.npad > 61 ? 1024u : 512u;
 
+  constexpr int bps = kBlocks;  // a stage: the blocks' weights, then their codes
+  const uint32_t codes_off = static_cast<uint32_t>(bps) * kMx4BlockBytes;
+  const uint32_t xs_slots = static_cast<uint32_t>(kXsSlots / bps);
+
   // Test build only (SPENSE_TEST_HOOKS): to exercise the failure path, the
   // loaders wait (bounded) on a word nothing sets, before any copy is issued.
   auto test_gate_wait = [&]() {
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     const uint64_t pol = p.w_keep ? ptx::policy_evict_normal() : ptx::policy_evict_first();
     TileWalker<kPair> walk(p, list);
     Ring ring(static_cast<uint32_t>(p.stages));
-    int i = 0;
+    int i = 0;  // stages filled
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
       // Pair mode: the pair's two weight tiles, one a CTA (past the last tile the
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
       const int wt = kPair ? min(2 * tile.n_tile + static_cast<int>(rank), p.n_tiles - 1) : tile.n_tile;
       const int wt0 = (tile.e * p.n_tiles + wt) * p.kblocks;  // the weight tile's first block
       const uint8_t* src = p.blocks + static_cast<size_t>(wt0) * kMx4BlockBytes;
-      for (int kb = kb0; kb < kb1; ++kb, ++i, ring.advance()) {
+      for (int kb = kb0; kb < kb1; kb += bps, ++i, ring.advance()) {
         if ((i & 1) != (warp & 1)) continue;
         ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
                       abort_flag);
@@ -367,8 +372,9 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
             if (rank == 0) ptx::mbar_arrive_expect_tx(full, 2 * kMx4BlockBytes);
             ptx::tma_load_2d_pair(dst, &maps.w, 0, (wt0 + kb) * (kMx4BlockBytes / 128), ptx::mapa(full, 0u), pol);
           } else {
-            ptx::mbar_arrive_expect_tx(full, kMx4BlockBytes);
-            ptx::bulk_g2s(dst, src + static_cast<size_t>(kb) * kMx4BlockBytes, kMx4BlockBytes, full, pol);
+            const uint32_t bytes = static_cast<uint32_t>(min(bps, kb1 - kb)) * kMx4BlockBytes;
+            ptx::mbar_arrive_expect_tx(full, bytes);
+            ptx::bulk_g2s(dst, src + static_cast<size_t>(kb) * kMx4BlockBytes, bytes, full, pol);
           }
         }
       }
@@ -390,13 +396,13 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
       const int b = rows <= p.box[0] ? 0 : (rows <= p.box[1] ? 1 : 2);
       const CUtensorMap* map = &maps.x[b];
       const uint32_t bytes = static_cast<uint32_t>(p.box[b]) * 128u;
-      for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
+      for (int kb = kb0; kb < kb1; kb += bps, ring.advance()) {
         ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
                       abort_flag);
         if (!ok) break;
         if (ptx::elect_one()) {
           const uint32_t full = ptx::smem_addr(&bars->full[ring.s]);
-          const uint32_t dst = smem_base + ring.s * p.stage_bytes + kMx4BlockBytes;
+          const uint32_t dst = smem_base + ring.s * p.stage_bytes + codes_off;
           if constexpr (kPair) {
             // The scales of all the tile's rows, in the tensor core's order, beside this CTA's half of the codes.
             const uint32_t full0 = ptx::mapa(full, 0u);
@@ -405,8 +411,11 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
             ptx::tma_load_2d_pair(dst + static_cast<uint32_t>(p.npad / 2) * 128u, &maps.xs_tiles, 0,
                                   (tile.row_tile * p.kblocks + kb) * (kMx4XsTileBytes / 128), full0, pol);
           } else {
-            ptx::mbar_arrive_expect_tx(full, bytes);
-            ptx::tma_load_2d(dst, map, kb * 128, row0, full, pol);
+            const int nb = min(bps, kb1 - kb);
+            ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(nb) * bytes);
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j)
+              if (j < nb) ptx::tma_load_2d(dst + static_cast<uint32_t>(j * p.npad) * 128u, map, (kb + j) * 128, row0, full, pol);
           }
         }
       }
@@ -422,22 +431,25 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     ptx::griddep_wait();
     const uint64_t pol = ptx::policy_evict_last();
     TileWalker<kPair> walk(p, list);
-    Ring ring(kXsSlots);
+    Ring ring(xs_slots);
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
-      for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
+      const bool wide = tile.rows > 61;  // up to three words in front of the tile's rows
+      const CUtensorMap* map = wide ? &maps.xs_wide : &maps.xs_narrow;
+      for (int kb = kb0; kb < kb1; kb += bps, ring.advance()) {
         ok = wait_all(ptx::smem_addr(&bars->xs_empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
                       abort_flag);
         if (!ok) break;
         if (ptx::elect_one()) {
           const uint32_t dst = xs_base + ring.s * p.xs_bytes, bar = ptx::smem_addr(&bars->xs_in[ring.s]);
-          const int g0 = 2 * kb, g1 = min(2 * kb + 1, p.groups - 1);  // past the last group the last one again, unused
-          const int x0 = (g0 * p.T + tile.row0) & ~3, x1 = (g1 * p.T + tile.row0) & ~3;
-          const bool wide = tile.rows > 61;  // up to three words in front of the tile's rows
-          ptx::mbar_arrive_expect_tx(bar, wide ? 2048u : 512u);
-          const CUtensorMap* map = wide ? &maps.xs_wide : &maps.xs_narrow;
-          ptx::tma_load_1d(dst, map, x0, bar, pol);
-          ptx::tma_load_1d(dst + group_bytes, map, x1, bar, pol);
+          const int ng = 2 * min(bps, kb1 - kb);
+          ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(ng) * (wide ? 1024u : 256u));
+#pragma unroll
+          for (int j = 0; j < 2 * kBlocks; ++j) {
+            if (j >= ng) break;
+            const int g = min(2 * kb + j, p.groups - 1);  // past the last group the last one again, unused
+            ptx::tma_load_1d(dst + static_cast<uint32_t>(j) * group_bytes, map, (g * p.T + tile.row0) & ~3, bar, pol);
+          }
         }
       }
     }
@@ -447,31 +459,33 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     // the memory operations the warp has in flight. Lane l takes rows l, 32 + l, ..
     // of both groups and writes them back as one 16-byte word per 128 rows.
     TileWalker<kPair> walk(p, list);
-    Ring ring(kXsSlots);
+    Ring ring(xs_slots);
     bool ok = true;
     for (int t = unit; ok && t < total; t += units) {
       const Tile tile = walk.get(t);
-      for (int kb = kb0; kb < kb1; ++kb, ring.advance()) {
+      for (int kb = kb0; kb < kb1; kb += bps, ring.advance()) {
         ok = wait_all(ptx::smem_addr(&bars->xs_in[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
                       abort_flag);
         if (!ok) break;
-        const uint32_t base = xs_base + ring.s * p.xs_bytes;
-        const uint32_t s0 = static_cast<uint32_t>(2 * kb * p.T + tile.row0) & 3u;
-        const uint32_t s1 = static_cast<uint32_t>(min(2 * kb + 1, p.groups - 1) * p.T + tile.row0) & 3u;
-        uint32_t w[2][8];
+        uint32_t base = xs_base + ring.s * p.xs_bytes;
+        for (int k = kb; k < min(kb + bps, kb1); ++k, base += 2u * group_bytes) {
+          const uint32_t s0 = static_cast<uint32_t>(2 * k * p.T + tile.row0) & 3u;
+          const uint32_t s1 = static_cast<uint32_t>(min(2 * k + 1, p.groups - 1) * p.T + tile.row0) & 3u;
+          uint32_t w[2][8];
 #pragma unroll
-        for (uint32_t q = 0; q < 8; ++q) {
-          if (32 * static_cast<int>(q) >= tile.rows) break;
-          const uint32_t at = base + (32u * q + static_cast<uint32_t>(lane)) * 4u;
-          w[0][q] = ptx::ld_smem_u32(at + 4u * s0);
-          w[1][q] = ptx::ld_smem_u32(at + 4u * s1 + group_bytes);
-        }
-        __syncwarp();
+          for (uint32_t q = 0; q < 8; ++q) {
+            if (32 * static_cast<int>(q) >= tile.rows) break;
+            const uint32_t at = base + (32u * q + static_cast<uint32_t>(lane)) * 4u;
+            w[0][q] = ptx::ld_smem_u32(at + 4u * s0);
+            w[1][q] = ptx::ld_smem_u32(at + 4u * s1 + group_bytes);
+          }
+          __syncwarp();
 #pragma unroll
-        for (uint32_t j = 0; j < 2; ++j) {
-          const uint32_t dst = base + j * group_bytes + static_cast<uint32_t>(lane) * 16u;
-          ptx::st_smem_u4(dst, w[j][0], w[j][1], w[j][2], w[j][3]);
-          if (tile.rows > 128) ptx::st_smem_u4(dst + 512u, w[j][4], w[j][5], w[j][6], w[j][7]);
+          for (uint32_t j = 0; j < 2; ++j) {
+            const uint32_t dst = base + j * group_bytes + static_cast<uint32_t>(lane) * 16u;
+            ptx::st_smem_u4(dst, w[j][0], w[j][1], w[j][2], w[j][3]);
+            if (tile.rows > 128) ptx::st_smem_u4(dst + 512u, w[j][4], w[j][5], w[j][6], w[j][7]);
+          }
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -484,9 +498,10 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     // flow the compiler knows to be uniform, the operands stay in uniform
     // registers, where these instructions want them.
     TileWalker<kPair> walk(p, list);
-    Ring ring(static_cast<uint32_t>(p.stages)), xring(kXsSlots);
+    Ring ring(static_cast<uint32_t>(p.stages)), xring(xs_slots);
     const uint32_t sf_base = tmem_base + static_cast<uint32_t>(p.nacc * p.npad);
     const uint32_t atoms = (static_cast<uint32_t>(p.npad) + 127u) >> 7;
+    const uint32_t sf_cols = 8u + 8u * atoms;  // of a block: weights' two column groups, activations' two
     uint32_t acc = 0, aph = 1;
     bool ok = !(kPair && rank == 1);  // the even CTA issues the pair's MMAs
     for (int t = unit; ok && t < total; t += units) {
@@ -497,22 +512,15 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * static_cast<uint32_t>(p.npad);
-      for (int kb = kb0; kb < kb1; ++kb, ring.advance(), xring.advance()) {
+      for (int kb = kb0; kb < kb1; kb += bps, ring.advance(), xring.advance()) {
         ok = (kPair || wait_all(ptx::smem_addr(&bars->xs_full[xring.s]), xring.ph, p.status,
                                 SPENSE_DEVICE_TIMEOUT_MMA, abort_flag)) &&
              wait_all(ptx::smem_addr(&bars->full[ring.s]), ring.ph, p.status, SPENSE_DEVICE_TIMEOUT_MMA, abort_flag);
         if (!ok) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
+          const int nb = min(bps, kb1 - kb);
           const uint32_t a_s = smem_base + ring.s * p.stage_bytes;
-          const uint64_t ad = ptx::desc_sw128(a_s), bd = ptx::desc_sw128(a_s + kMx4BlockBytes);
-          const uint64_t wd = ptx::desc_rows16(a_s + kMx4CodeBytes), xd = ptx::desc_rows16(
-              kPair ? a_s + kMx4BlockBytes + static_cast<uint32_t>(p.npad / 2) * 128u : xs_base + xring.s * p.xs_bytes);
-          // Scales: 8 columns for the weights' two column groups, then 4 or 8 a group for
-          // the activations. Every stage has columns of its own, so that the stage's
-          // refill says that the products that read them have completed.
-          const uint32_t sfa = sf_base + ring.s * (8u + 8u * atoms), sfb = sfa + 8u;
-          const uint32_t steps = kb + 1 == p.kblocks ? static_cast<uint32_t>(p.last_steps) : 4u;
           auto cp = [](uint32_t taddr, uint64_t desc) {
             if constexpr (kPair)
               ptx::tmem_cp_32x128b_x4_pair(taddr, desc);
@@ -525,24 +533,45 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
             else
               ptx::mma_commit(ptx::smem_addr(bar));
           };
+          // Every stage has scale columns of its own, so that the stage's refill says
+          // that the products that read them have completed.
+          const uint32_t sf_stage = sf_base + ring.s * static_cast<uint32_t>(bps) * sf_cols;
 #pragma unroll
-          for (uint32_t j = 0; j < 2; ++j) {
-            cp(sfa + 4u * j, wd + 32u * j);
-            cp(sfb + 4u * atoms * j, xd + j * (group_bytes >> 4));
-            if (atoms > 1) cp(sfb + 4u * atoms * j + 4u, xd + j * (group_bytes >> 4) + 32u);
+          for (int b = 0; b < kBlocks; ++b) {
+            if (b >= nb) break;
+            const uint64_t wd = ptx::desc_rows16(a_s + static_cast<uint32_t>(b) * kMx4BlockBytes + kMx4CodeBytes);
+            const uint64_t xd = ptx::desc_rows16(kPair ? a_s + kMx4BlockBytes + static_cast<uint32_t>(p.npad / 2) * 128u
+                                                       : xs_base + xring.s * p.xs_bytes +
+                                                             static_cast<uint32_t>(b) * 2u * group_bytes);
+            const uint32_t sfa = sf_stage + static_cast<uint32_t>(b) * sf_cols, sfb = sfa + 8u;
+#pragma unroll
+            for (uint32_t j = 0; j < 2; ++j) {
+              cp(sfa + 4u * j, wd + 32u * j);
+              cp(sfb + 4u * atoms * j, xd + j * (group_bytes >> 4));
+              if (atoms > 1) cp(sfb + 4u * atoms * j + 4u, xd + j * (group_bytes >> 4) + 32u);
+            }
           }
           if constexpr (!kPair) commit(&bars->xs_empty[xring.s]);
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k) {
-            if (k >= steps) break;
-            const uint32_t id = idesc ^ ((k & 1u) ? sf2 : 0u), accum = (kb > kb0 || k > 0) ? 1u : 0u;
-            if constexpr (kPair)
-              ptx::mma_mxf4_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, sfa + 4u * (k >> 1), sfb + 4u * atoms * (k >> 1), accum);
-            else
-              ptx::mma_mxf4(d_tmem, ad + 2u * k, bd + 2u * k, id, sfa + 4u * (k >> 1), sfb + 4u * atoms * (k >> 1), accum);
+          for (int b = 0; b < kBlocks; ++b) {
+            if (b >= nb) break;
+            const uint64_t ad = ptx::desc_sw128(a_s + static_cast<uint32_t>(b) * kMx4BlockBytes);
+            const uint64_t bd = ptx::desc_sw128(a_s + codes_off + static_cast<uint32_t>(b * p.npad) * 128u);
+            const uint32_t sfa = sf_stage + static_cast<uint32_t>(b) * sf_cols, sfb = sfa + 8u;
+            const uint32_t steps = kb + b + 1 == p.kblocks ? static_cast<uint32_t>(p.last_steps) : 4u;
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+              if (k >= steps) break;
+              const uint32_t id = idesc ^ ((k & 1u) ? sf2 : 0u), accum = (kb + b > kb0 || k > 0) ? 1u : 0u;
+              const uint32_t fa = sfa + 4u * (k >> 1), fb = sfb + 4u * atoms * (k >> 1);
+              if constexpr (kPair)
+                ptx::mma_mxf4_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, fa, fb, accum);
+              else
+                ptx::mma_mxf4(d_tmem, ad + 2u * k, bd + 2u * k, id, fa, fb, accum);
+            }
           }
           commit(&bars->empty[ring.s]);
-          if (kb + 1 == kb1) commit(&bars->acc_full[acc]);
+          if (kb + bps >= kb1) commit(&bars->acc_full[acc]);
         }
         __syncwarp();
       }
@@ -764,10 +793,11 @@ cudaError_t allow_smem() {
   int dev = 0;
   cudaError_t st = cudaGetDevice(&dev);
   if (st != cudaSuccess || configured_for == dev) return st;
-  st = cudaFuncSetAttribute(spense_mx4_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-  if (st == cudaSuccess)
-    st = cudaFuncSetAttribute(spense_mx4_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-  if (st == cudaSuccess) configured_for = dev;
+  for (auto f : {spense_mx4_gemm_kernel<false, 1>, spense_mx4_gemm_kernel<false, 2>, spense_mx4_gemm_kernel<true, 1>}) {
+    st = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (st != cudaSuccess) return st;
+  }
+  configured_for = dev;
   return st;
 }
 
@@ -798,7 +828,7 @@ cudaError_t mx4_max_clusters(int cluster, uint32_t smem_bytes, int* out) {
   if (st != cudaSuccess) return st;
   cudaLaunchAttribute attr[3];
   const cudaLaunchConfig_t cfg = gemm_config(cluster, cluster, smem_bytes, nullptr, attr);
-  return cudaOccupancyMaxActiveClusters(out, spense_mx4_gemm_kernel<false>, &cfg);
+  return cudaOccupancyMaxActiveClusters(out, spense_mx4_gemm_kernel<false, 1>, &cfg);
 }
 
 cudaError_t launch_mx4_gemm(const Mx4GemmMaps& maps, const Mx4GemmParams& p, int grid, uint32_t smem_bytes,
@@ -807,8 +837,9 @@ cudaError_t launch_mx4_gemm(const Mx4GemmMaps& maps, const Mx4GemmParams& p, int
   if (st != cudaSuccess) return st;
   cudaLaunchAttribute attr[3];
   const cudaLaunchConfig_t cfg = gemm_config(grid, p.pair ? 2 : p.split, smem_bytes, stream, attr);
-  return p.pair ? cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<true>, maps, p)
-                : cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<false>, maps, p);
+  if (p.pair) return cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<true, 1>, maps, p);
+  return p.bps == 2 ? cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<false, 2>, maps, p)
+                    : cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<false, 1>, maps, p);
 }
 
 }  // namespace spense

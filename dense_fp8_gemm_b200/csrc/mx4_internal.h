@@ -38,6 +38,7 @@ struct Mx4GemmParams {
   int npad;                // rows of activations per tile (MMA N), a multiple of 16
   int box[3];              // rows one activation load covers, smallest first; box[2]: a CTA's share of npad
   int stages, nacc;
+  int bps;                 // blocks a stage holds (1 or 2)
   int pair;                // 1: CTA pairs (tcgen05 cta_group::2) share 256-row MMAs
   int split;               // CTAs of a cluster sharing one tile's K range (1: none)
   uint32_t stage_bytes, xs_bytes, tmem_cols;  // bytes of a stage, of a slot of activation scales
@@ -55,7 +56,7 @@ struct Mx4GemmMaps {
 constexpr int kMx4MaxTile = 240;  // rows a tile takes: with three words in front, one box of 256 scale words
 
 struct Mx4GemmPlan {
-  int npad, stages, nacc, pair, split, ctas_per_sm, grid;
+  int npad, stages, nacc, bps, pair, split, ctas_per_sm, grid;
   int64_t row_tiles;  // row tiles at most (all experts)
   size_t workspace_bytes;
   uint32_t stage_bytes, xs_bytes, tmem_cols, smem_bytes;
