@@ -115,20 +115,53 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int i = 0; i < Q::kPieces; ++i) {
     const int c = col0 + 512 * i;
-    float f[16];
-    to_floats<kType, kLoads>(raw[i], f);
-    // Magnitudes as bit patterns: ordered like the values, infinities and NaN above all.
-    uint32_t m = 0;
+    // The largest magnitude of the thread's 16 values as a float's bit pattern:
+    // patterns are ordered like the values, infinities and NaN above all. 16-bit
+    // types compare their own patterns, two at a time.
+    uint32_t m;
+    if constexpr (kType == SPENSE_TYPE_F32) {
+      m = 0u;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+      for (int j = 0; j < kLoads; ++j)
+        m = max(max(m, max(raw[i][j].x & 0x7FFFFFFFu, raw[i][j].y & 0x7FFFFFFFu)),
+                max(raw[i][j].z & 0x7FFFFFFFu, raw[i][j].w & 0x7FFFFFFFu));
+    } else {
+      uint32_t p = 0u;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+        p = __vmaxu2(__vmaxu2(p, __vmaxu2(raw[i][j].x & 0x7FFF7FFFu, raw[i][j].y & 0x7FFF7FFFu)),
+                     __vmaxu2(raw[i][j].z & 0x7FFF7FFFu, raw[i][j].w & 0x7FFF7FFFu));
+      p = max(p & 0xFFFFu, p >> 16);
+      m = kType == SPENSE_TYPE_BF16 ? p << 16
+                                    : __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(p))));
+    }
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     // Scale byte e + 127 = (biased exponent of the largest magnitude) - 2, from
     // below cut at 0 (zeros, subnormals); 255 marks a block that is not finite.
     const uint32_t ex = m >> 23;
     const uint32_t byte = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
-    const float inv = __uint_as_float(byte == 255u ? 0x3F800000u : (254u - byte) << 23);  // 2^-e
+    const uint32_t inv = byte == 255u ? 0x3F800000u : (254u - byte) << 23;  // 2^-e as a float
+    float f[16];
+    if constexpr (kType == SPENSE_TYPE_BF16) {
+      // 2^-e and x 2^-e are bf16 values (its exponents are fp32's): two products at once.
+      const uint32_t two = inv | (inv >> 16);
+      const __nv_bfloat162 inv2 = *reinterpret_cast<const __nv_bfloat162*>(&two);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) f[j] *= inv;
+      for (int j = 0; j < kLoads; ++j) {
+        const uint32_t w[4] = {raw[i][j].x, raw[i][j].y, raw[i][j].z, raw[i][j].w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[h]), inv2);
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
+          f[8 * j + 2 * h] = __uint_as_float(u << 16);
+          f[8 * j + 2 * h + 1] = __uint_as_float(u & 0xFFFF0000u);
+        }
+      }
+    } else {
+      to_floats<kType, kLoads>(raw[i], f);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] *= __uint_as_float(inv);
+    }
     const bool live = src >= 0 && c < K;
     if (live)
       *reinterpret_cast<uint2*>(Xq + (static_cast<int64_t>(row) * K + c) / 2) =

@@ -68,6 +68,20 @@ def test_quantize_extremes():
         assert np.array_equal(y, want, equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows", [7, 4000])
+def test_quantize_every_bit_pattern(dtype, rows):
+    """All 65536 patterns of a 16-bit type (subnormals, infinities and NaN among
+    them), in blocks of neighbouring patterns and in shuffled ones."""
+    bits = np.arange(65536, dtype=np.uint16)
+    shuffled = np.random.default_rng(1).permutation(bits)
+    both = np.concatenate((bits, shuffled)).reshape(-1, 256)
+    x = torch.from_numpy(np.resize(both, (max(rows, 512), 256))[:rows if rows < 512 else None].view(np.int16).copy())
+    X = x.cuda().view(DTYPES[dtype])
+    q, s = spense.mx4_quantize(X)
+    check_quantised(X, q, s)
+
+
 @pytest.mark.parametrize("M,K", [(1, 32), (5, 160), (40, 1056), (300, 4096)])
 @pytest.mark.parametrize("scale_rows", [False, True])
 def test_dequantize_every_code(M, K, scale_rows):
