@@ -2,10 +2,9 @@
 // packed handle and launch planning.
 #include <algorithm>
 #include <array>
+#include <atomic>
 #include <climits>
 #include <cstdlib>
-#include <map>
-#include <mutex>
 #include <new>
 
 #include "abi_util.h"
@@ -29,16 +28,14 @@ constexpr uint32_t kMx4Smem[2] = {232448u, 115200u};
 
 // Clusters of s CTAs, cps to a SM, that the device holds at once.
 int clusters_at_once(int s, int cps, int sms) {
-  static std::mutex mu;
-  static std::map<std::array<int, 3>, int> known;
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][9][3];  // the number + 1; 0: not asked yet
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return sms * cps / (s + 1);
-  std::lock_guard<std::mutex> lk(mu);
-  const auto it = known.find({dev, s, cps});
-  if (it != known.end()) return it->second;
+  if (dev < kDevices && known[dev][s][cps] > 0) return known[dev][s][cps] - 1;
   int n = 0;
   if (mx4_max_clusters(s, kMx4Smem[cps - 1], &n) != cudaSuccess) n = sms * cps / (s + 1);
-  known[{dev, s, cps}] = n;
+  if (dev < kDevices) known[dev][s][cps] = n + 1;
   return n;
 }
 

@@ -362,6 +362,8 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
       const uint8_t* src = p.blocks + static_cast<size_t>(wt0) * kMx4BlockBytes;
       for (int kb = kb0; kb < kb1; kb += bps, ++i, ring.advance()) {
         if ((i & 1) != (warp & 1)) continue;
+        // Nothing is consumed while the previous grid runs, however long that takes.
+        if (i >= p.stages && i < p.stages + 2) ptx::griddep_wait();
         ok = wait_all(ptx::smem_addr(&bars->empty[ring.s]), ring.ph ^ 1u, p.status, SPENSE_DEVICE_TIMEOUT_PRODUCER,
                       abort_flag);
         if (!ok) break;
@@ -458,6 +460,7 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     // A warp of its own: the fence in front of the tensor core's reads waits for
     // the memory operations the warp has in flight. Lane l takes rows l, 32 + l, ..
     // of both groups and writes them back as one 16-byte word per 128 rows.
+    ptx::griddep_wait();
     TileWalker<kPair> walk(p, list);
     Ring ring(xs_slots);
     bool ok = true;
@@ -497,6 +500,7 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     // The whole warp walks the blocks and one elected lane issues: with control
     // flow the compiler knows to be uniform, the operands stay in uniform
     // registers, where these instructions want them.
+    ptx::griddep_wait();  // no bounded wait begins before the activations can come
     TileWalker<kPair> walk(p, list);
     Ring ring(static_cast<uint32_t>(p.stages)), xring(xs_slots);
     const uint32_t sf_base = tmem_base + static_cast<uint32_t>(p.nacc * p.npad);

@@ -627,11 +627,12 @@ def mx4_quantize(X: torch.Tensor, rows: torch.Tensor | None = None, scale_rows: 
     x, ldx = _rows_addr(X, dtype, dev, "X", M, K)
     T, r = (M, None) if rows is None else (rows.shape[0], _addr(rows, torch.int32, dev, "rows"))
     if Xq is None:
-        Xq = torch.empty((T, K // 2), dtype=torch.uint8, device=X.device)
+        Xq = torch.empty(T, K // 2, dtype=torch.uint8, device=X.device)
     elif Xq.shape != (T, K // 2):
         raise ValueError(f"Xq must be [{T}, {K // 2}], got {tuple(Xq.shape)}")
     if x_scale is None:
-        x_scale = torch.empty((T, K // 32) if scale_rows else (-(-K // 128), T, 4), dtype=torch.uint8, device=X.device)
+        x_scale = torch.empty(*((T, K // 32) if scale_rows else (-(-K // 128), T, 4)), dtype=torch.uint8,
+                              device=X.device)
     elif scale_rows and x_scale.shape != (T, K // 32):
         raise ValueError(f"x_scale must be [{T}, {K // 32}], got {tuple(x_scale.shape)}")
     flags = MX4_SCALE_ROWS if scale_rows else _scale_flags(x_scale, T, K)
@@ -652,7 +653,7 @@ def mx4_dequantize(Xq: torch.Tensor, x_scale: torch.Tensor, dtype=torch.bfloat16
     M, K = Xq.shape
     K *= 2
     if out is None:
-        out = torch.empty((M, K), dtype=dtype, device=Xq.device)
+        out = torch.empty(M, K, dtype=dtype, device=Xq.device)
     if out.shape != (M, K) or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"the output must be bfloat16 or float32 [{M}, {K}], got {out.dtype} {tuple(out.shape)}")
     code = lib().spense_mx4_dequantize(_addr(Xq, torch.uint8, dev, "Xq"), _addr(x_scale, torch.uint8, dev, "x_scale"),
@@ -812,7 +813,8 @@ def expert_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, 
         need = _sort_workspace(M, k, E) // 4
         if need == 0:
             _check(2, "spense_expert_sort")
-        ws, r, p, o = torch.empty(need + 2 * n + E + 1, dtype=torch.int32, device=ids.device).split((need, n, n, E + 1))
+        made = torch.empty(need + 2 * n + E + 1, dtype=torch.int32, device=ids.device)
+        ws, r, p, o = made.split_with_sizes((need, n, n, E + 1))
         workspace = ws if workspace is None else workspace
         rows = r if rows is None else rows
         pos = p.view(M, k) if pos is None else pos
@@ -842,7 +844,7 @@ def expert_combine(Y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, ou
     M, k = pos.shape
     y, ldy = _rows_addr(Y, torch.bfloat16, dev, "Y", T, N)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=Y.device)
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=Y.device)
     elif out.shape != (M, N):
         raise ValueError(f"out must be [{M}, {N}], got {tuple(out.shape)}")
     o, ldo = _rows_addr(out, torch.bfloat16, dev, "out", M, N)
