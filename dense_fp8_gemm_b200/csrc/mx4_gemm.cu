@@ -186,10 +186,22 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // apart) that leave each lane with eight consecutive weight rows (8 (l / 8) ..) of
 // activation row c + l % 8 of every eight: one 16-byte store a group, 64
 // contiguous bytes a row, without shared memory. The rounds of all groups are
-// interleaved to cover the exchanges' latency.
+// interleaved to cover the exchanges' latency. Where rows of Y are not 16-byte
+// aligned, or end in these 32, every lane stores its own values instead, 2 bytes
+// each, a warp 64 contiguous bytes of a row.
 template <int kGroups>
 __device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y, int64_t ldy, int c, int rows,
                                            int n_warp, int N) {
+  if (n_warp + 32 > N || (ldy & 7) != 0) {
+    const int n = n_warp + lane;
+    uint16_t* dst = y + c * ldy + n;
+    if (n < N)
+#pragma unroll
+      for (int i = 0; i < 8 * kGroups; ++i, dst += ldy)
+        if (c + i < rows) *dst = __bfloat16_as_ushort(__float2bfloat16_rn(a[i]));
+    __syncwarp();
+    return;
+  }
   const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
   uint32_t q[kGroups][4];
 #pragma unroll
@@ -209,6 +221,8 @@ __device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y
       r[g][2 * i] = b1 ? o : q[g][2 * i];
       r[g][2 * i + 1] = b1 ? q[g][2 * i + 1] : o;
     }
+  const int m = c + (lane & 7);
+  uint16_t* dst = y + m * ldy + n_warp + (lane >> 3) * 8;
   uint4 v[kGroups];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
@@ -216,22 +230,9 @@ __device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y
     const uint32_t o1 = __shfl_xor_sync(0xffffffffu, b2 ? r[g][1] : r[g][3], 4);
     v[g] = b2 ? make_uint4(o0, o1, r[g][2], r[g][3]) : make_uint4(r[g][0], r[g][1], o0, o1);
   }
-  const int m = c + (lane & 7), n = n_warp + (lane >> 3) * 8;
-  uint16_t* dst = y + m * ldy + n;
-  if (n_warp + 32 <= N && (ldy & 7) == 0) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g, dst += 8 * ldy)
-      if (m + 8 * g < rows) ptx::st_global_v4(dst, v[g]);
-  } else {
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g, dst += 8 * ldy) {
-      const uint32_t w[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
-      if (m + 8 * g < rows)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < N) dst[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-    }
-  }
+  for (int g = 0; g < kGroups; ++g, dst += 8 * ldy)
+    if (m + 8 * g < rows) ptx::st_global_v4(dst, v[g]);
 }
 
 // kBlocks: blocks a stage holds.

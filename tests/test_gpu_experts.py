@@ -47,7 +47,8 @@ def test_sort_of_nothing():
 
 
 @pytest.mark.parametrize("M,k,N,drop", [(1, 1, 1, 0.0), (3, 2, 8, 0.0), (5, 8, 1000, 0.3), (17, 9, 129, 0.2),
-                                        (64, 4, 2560, 0.0), (200, 6, 1023, 0.5), (9, 64, 72, 0.9), (4, 3, 264, 1.0)])
+                                        (64, 4, 2560, 0.0), (200, 6, 1023, 0.5), (9, 64, 72, 0.9), (4, 3, 264, 1.0),
+                                        (7, 3, 513, 0.1), (6, 5, 1307, 0.2), (33, 1, 1026, 0.0), (5, 2, 2047, 0.3)])
 def test_combine(M, k, N, drop):
     g = np.random.default_rng(M + N)
     T = M * k
