@@ -21,6 +21,7 @@ constexpr int kMx4BlockBytes = kMx4CodeBytes + kMx4ScaleBytes;
 constexpr int kMx4BarrierBytes = 512;  // mbarriers and flags behind the ring
 constexpr int kMx4XsSlots = 8;  // blocks whose activation scales are ahead of the products
 constexpr int kMx4XsTileBytes = 2048;  // scales of a block for up to 256 rows, in tcgen05.cp's order
+constexpr int kMx4RowGroup = 12;  // row tiles that all weight tiles pass before the next ones
 constexpr int kMx4MaxExperts = 1024;
 constexpr int64_t kMx4MaxRows = 1 << 20;
 
