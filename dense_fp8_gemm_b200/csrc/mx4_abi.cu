@@ -278,6 +278,12 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
   const int tail_cols = static_cast<int>(h->K - static_cast<int64_t>(h->kblocks - 1) * kMx4Cols);
   p.last_steps = (tail_cols + 63) / 64;
   p.npad = pl.npad;
+  // Activation codes of up to 32 MB stay in L2 while all weights pass, and the weights
+  // are read once (51200x5120 at 8192 rows 998 us, in groups of 12 row tiles 1042 us, at
+  // the power cap). More of them go in groups of 16 row tiles: 20480x5120 at 65536 rows
+  // 3490 -> 3130 us, 5120x27648 at 16384 rows 1223 -> 1033 us, 5120x5120 at 32768 rows 438
+  // -> 400 us.
+  p.group = T * (h->K / 2) <= (32 << 20) ? 1 << 16 : 16;
   p.stages = pl.stages;
   p.nacc = pl.nacc;
   p.bps = pl.bps;

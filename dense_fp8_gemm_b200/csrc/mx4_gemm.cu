@@ -153,18 +153,15 @@ struct TileWalker {
     while (t >= list.tile_begin[e + 1]) ++e;
     const int local = t - list.tile_begin[e];
     const int cnt = list.count[e];
-    // Row tiles in groups, a group's row tiles of one weight tile next to each other:
-    // the tiles that run at one time then form a block of some 12 row tiles by 6 to 12
-    // weight tiles, which reads the fewest different bytes, and a group's codes stay in
-    // L2 while the weights pass. 20480x5120 at 65536 rows 3490 (all row tiles) -> 3135
-    // us, 5120x27648 at 16384 rows 1223 -> 1013 us.
+    // Row tiles in groups of p.group: those of one weight tile next to each other, then
+    // the next weight tile's, so that a group's codes stay in L2 while the weights pass.
     const int m_tiles = (cnt + p.npad - 1) / p.npad;
-    const int per_group = kMx4RowGroup * weight_tiles<kPair>(p);
+    const int per_group = p.group * weight_tiles<kPair>(p);
     const int group = local / per_group;
     const int in_group = local - group * per_group;
-    const int size = min(kMx4RowGroup, m_tiles - group * kMx4RowGroup);
+    const int size = min(p.group, m_tiles - group * p.group);
     const int nt = in_group / size;
-    const int r = (group * kMx4RowGroup + in_group - nt * size) * p.npad;
+    const int r = (group * p.group + in_group - nt * size) * p.npad;
     return Tile{__shfl_sync(0xffffffffu, e, 0), __shfl_sync(0xffffffffu, nt, 0),
                 __shfl_sync(0xffffffffu, list.first[e] + r, 0), __shfl_sync(0xffffffffu, min(p.npad, cnt - r), 0),
                 __shfl_sync(0xffffffffu, list.tile_begin[e] / weight_tiles<kPair>(p) + r / p.npad, 0)};

@@ -21,7 +21,6 @@ constexpr int kMx4BlockBytes = kMx4CodeBytes + kMx4ScaleBytes;
 constexpr int kMx4BarrierBytes = 512;  // mbarriers and flags behind the ring
 constexpr int kMx4XsSlots = 8;  // blocks whose activation scales are ahead of the products
 constexpr int kMx4XsTileBytes = 2048;  // scales of a block for up to 256 rows, in tcgen05.cp's order
-constexpr int kMx4RowGroup = 12;  // row tiles that all weight tiles pass before the next ones
 constexpr int kMx4MaxExperts = 1024;
 constexpr int64_t kMx4MaxRows = 1 << 20;
 
@@ -38,6 +37,7 @@ struct Mx4GemmParams {
   int last_steps;          // K = 64 steps in the last block (1 .. 4)
   int npad;                // rows of activations per tile (MMA N), a multiple of 16
   int box[3];              // rows one activation load covers, smallest first; box[2]: a CTA's share of npad
+  int group;               // row tiles that all weight tiles pass before the next ones
   int stages, nacc;
   int bps;                 // blocks a stage holds (1 or 2)
   int pair;                // 1: CTA pairs (tcgen05 cta_group::2) share 256-row MMAs
