@@ -4,7 +4,7 @@
 // are read from tensor memory beside the accumulator).
 //
 // Weight rows are the MMA M dimension (128 a tile), activation rows the MMA N
-// dimension (a multiple of 16, at most 256 a tile), so a decoding batch wastes
+// dimension (a multiple of 16, at most 240 a tile), so a decoding batch wastes
 // no tensor rows and a weight is read once for all the rows of a tile. With
 // offsets, expert e's weights meet rows offsets[e] .. offsets[e + 1] only; every
 // CTA makes the list of tiles from the offsets itself (they are known on the
@@ -27,6 +27,19 @@
 // Few tiles (p.split > 1): the CTAs of a cluster split a tile's K range, exchange
 // their fp32 partials through shared memory and finish a share of the tile's rows
 // each, adding the partials in rank order: the result does not depend on timing.
+//
+// Large products (kPair): two CTAs on two SMs share MMAs of 256 weight rows
+// (cta_group::2), each with its own 128 weight rows and half of the activation rows,
+// which cuts the bytes a flop moves into shared memory by a third. All copies of a
+// pair are counted on the even CTA's barriers; the scales come in the tensor core's
+// order from a launch in front.
+//
+// Bound: up to some 250 rows by the weights' way from HBM (0.53 bytes an element:
+// 64 experts 2560x5120 at 32 rows 36.2 us, 0.88 of the measured copy rate; 128
+// experts 2560x2048 at 509 rows 59.3 us, 0.92), for few weights by the 3.2 us around
+// the blocks and a CTA's 0.25 us a block (10240x5120 at one row 7.5 us), beyond by the
+// tensor pipe and the power cap (51200x5120 at 8192 rows 925 us, 4.6 PFLOP/s at a clock
+// of 1.17 GHz).
 //
 // Every wait is bounded (1.5 s); on expiry the kernel records a code in the
 // workspace's status word and all roles leave their loops.

@@ -64,8 +64,9 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* f) {
 //   kWide (many rows): the eight warps of a CTA take eight rows and each two such
 //     pieces of its row, all loads first. The CTA's scale words leave through
 //     shared memory, eight rows' words of a column group (32 bytes) at a time:
-//     written one by one they were twice as many requests as the codes (32768
-//     gathered rows of 5120 with eight columns a thread: 90 us; now 64).
+//     written one by one they were twice as many requests as the codes. 32768
+//     gathered rows of 5120 take 55 us (the rows' four readings from L2 bound it; with
+//     eight columns a thread and single words 90 us), 8192 rows in order 18 us.
 //   else (few rows): the eight warps take eight pieces of one row, so a token's
 //     5120 columns are two CTAs with one round of loads.
 template <bool kWide>
@@ -218,7 +219,7 @@ __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&v)[8]) 
 // Dequantiser. A thread takes 16 columns (half a block: one scale, 32 bytes of bf16
 // output in one store when the output is 32-byte aligned), a warp 512 columns of a
 // row; kWide: eight rows a CTA, two pieces a warp, all loads first; else eight
-// pieces of one row.
+// pieces of one row. 32768 rows of 5120 take 71 us, 6.0 TB/s (16-byte stores 86 us).
 //
 // Every value is exact in the output type (three significant bits; 2^-128 at
 // least) up to 6 x 2^125; larger ones, which the quantiser never makes, may
