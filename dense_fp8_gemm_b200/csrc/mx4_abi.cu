@@ -82,7 +82,7 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
   const double flops = 2.0 * T * n_tiles * kMx4Rows * kblocks * kMx4Cols;
   const int64_t avg = (T + E - 1) / E;
   pl.pair = flops >= 4e11 && kblocks >= 10 && (!ragged || avg >= 512) ? 1 : 0;
-  const int most = pl.pair ? 192 : kMx4MaxTile, step = pl.pair ? 32 : 16;
+  const int most = pl.pair ? kMx4PairRows : kMx4MaxTile, step = pl.pair ? 32 : 16;
   // Row tiles at most: every expert's last one may be short.
   auto row_tiles = [&](int n) { return ragged ? active + T / n : (T + n - 1) / n; };
   auto stage = [&](int n) {

@@ -10,7 +10,7 @@
 // CTA makes the list of tiles from the offsets itself (they are known on the
 // device only) and takes every gridDim-th tile.
 //
-// Roles (320 threads):
+// Roles (320 threads, a pair's CTAs 384):
 //   warps 0-3 epilogue: tensor memory -> registers -> bf16 rows of Y;
 //   warp 4    one lane copies the scales into tensor memory (tcgen05.cp) and
 //             issues four K = 64 MMAs a block;
@@ -32,7 +32,8 @@
 // (cta_group::2), each with its own 128 weight rows and half of the activation rows,
 // which cuts the bytes a flop moves into shared memory by a third. All copies of a
 // pair are counted on the even CTA's barriers; the scales come in the tensor core's
-// order from a launch in front.
+// order from a launch in front. Warps 8-11 are a second set of epilogue warps: a
+// tile's MMAs of 10 blocks take as long as one set needs for its 192 rows.
 //
 // Bound: up to some 250 rows by the weights' way from HBM (0.53 bytes an element:
 // 64 experts 2560x5120 at 32 rows 36.2 us, 0.88 of the measured copy rate; 128
@@ -57,6 +58,7 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 1500000000ull;
 constexpr int kMaxMx4Stages = 12;
 constexpr int kMx4Threads = 320;
+constexpr int kMx4PairThreads = 384;
 constexpr int kXsSlots = kMx4XsSlots;
 
 struct alignas(16) Mx4Barriers {
@@ -198,8 +200,8 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 // Stores a warp's 32 weight rows x (8 kGroups) activation rows. Lane l holds the
-// fp32 sums of its weight row, n_warp + l, for activation rows c .. c + 8 kGroups -
-// 1. As bf16 pairs they go through three exchange rounds (with lanes 1, 2 and 4
+// bf16 pairs of its weight row, n_warp + l, for activation rows c .. c + 8 kGroups -
+// 1. They go through three exchange rounds (with lanes 1, 2 and 4
 // apart) that leave each lane with eight consecutive weight rows (8 (l / 8) ..) of
 // activation row c + l % 8 of every eight: one 16-byte store a group, 64
 // contiguous bytes a row, without shared memory. The rounds of all groups are
@@ -207,15 +209,15 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // aligned, or end in these 32, every lane stores its own values instead, 2 bytes
 // each, a warp 64 contiguous bytes of a row.
 template <int kGroups>
-__device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y, int64_t ldy, int c, int rows,
-                                           int n_warp, int N) {
+__device__ __forceinline__ void store_pairs(const uint32_t* a, int lane, uint16_t* y, int64_t ldy, int c, int rows,
+                                            int n_warp, int N) {
   if (n_warp + 32 > N || (ldy & 7) != 0) {
     const int n = n_warp + lane;
     uint16_t* dst = y + c * ldy + n;
     if (n < N)
 #pragma unroll
       for (int i = 0; i < 8 * kGroups; ++i, dst += ldy)
-        if (c + i < rows) *dst = __bfloat16_as_ushort(__float2bfloat16_rn(a[i]));
+        if (c + i < rows) *dst = static_cast<uint16_t>(i & 1 ? a[i / 2] >> 16 : a[i / 2] & 0xffffu);
     __syncwarp();
     return;
   }
@@ -225,7 +227,7 @@ __device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y
   for (int g = 0; g < kGroups; ++g)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t v = bf16x2(a[8 * g + 2 * j], a[8 * g + 2 * j + 1]);
+      const uint32_t v = a[4 * g + j];
       const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 1);
       q[g][j] = b0 ? __byte_perm(o, v, 0x7632) : __byte_perm(v, o, 0x5410);
     }
@@ -252,9 +254,19 @@ __device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y
     if (m + 8 * g < rows) ptx::st_global_v4(dst, v[g]);
 }
 
+// The same of fp32 sums.
+template <int kGroups>
+__device__ __forceinline__ void store_rows(const float* a, int lane, uint16_t* y, int64_t ldy, int c, int rows,
+                                           int n_warp, int N) {
+  uint32_t pairs[4 * kGroups];
+#pragma unroll
+  for (int i = 0; i < 4 * kGroups; ++i) pairs[i] = bf16x2(a[2 * i], a[2 * i + 1]);
+  store_pairs<kGroups>(pairs, lane, y, ldy, c, rows, n_warp, N);
+}
+
 // kBlocks: blocks a stage holds.
 template <bool kPair, int kBlocks>
-__global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
+__global__ void __launch_bounds__(kPair ? kMx4PairThreads : kMx4Threads, kPair ? 1 : 2)
     spense_mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const __grid_constant__ Mx4GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -291,7 +303,7 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(ptx::smem_addr(&bars->acc_full[a]), 1);
       // pair mode: the odd CTA's epilogue arrives once, remotely
-      ptx::mbar_init(ptx::smem_addr(&bars->acc_empty[a]), kPair ? 129 : 128);
+      ptx::mbar_init(ptx::smem_addr(&bars->acc_empty[a]), kPair ? 257 : 128);
     }
     bars->abort_flag = 0;
     ptx::fence_mbar_init();
@@ -367,7 +379,9 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
     test_gate_wait();
     __syncwarp();
     bool ok = __all_sync(0xffffffffu, !*abort_flag);
-    const uint64_t pol = p.w_keep ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+    // Read again by later tiles: kept like the activations (5120x27648 at 16384 rows
+    // 1028 us as normal lines, 1006 so).
+    const uint64_t pol = p.w_keep ? ptx::policy_evict_last() : ptx::policy_evict_first();
     TileWalker<kPair> walk(p, list);
     Ring ring(static_cast<uint32_t>(p.stages));
     int i = 0;  // stages filled
@@ -602,24 +616,65 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
         aph ^= 1u;
       }
     }
-  } else if (warp < 4) {
+  } else if (warp < 4 || (kPair && warp >= 8)) {
     // ------------------------------------------------------------ epilogue
+    constexpr int kEpilogueThreads = kPair ? 256 : 128;
+    const int quarter = warp & 3;  // the lanes of tensor memory a warp may read
     ptx::griddep_wait();  // Y may be the previous grid's
     TileWalker<kPair> walk(p, list);
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     int u = 0;
     for (int t = unit; t < total; t += units, ++u) {
       const Tile tile = walk.get(t);
       const uint32_t acc = static_cast<uint32_t>(u % p.nacc), aph = static_cast<uint32_t>((u / p.nacc) & 1);
-      if (!ptx::named_bar_and(1, 128,
+      if (!ptx::named_bar_and(1, kEpilogueThreads,
                               wait_bar(ptx::smem_addr(&bars->acc_full[acc]), aph, p.status,
                                        SPENSE_DEVICE_TIMEOUT_EPILOGUE, abort_flag)))
         break;
       ptx::tc_fence_after();
       const uint32_t taddr = lane_base + acc * static_cast<uint32_t>(p.npad);
-      const int n_warp = (kPair ? 2 * tile.n_tile + static_cast<int>(rank) : tile.n_tile) * kMx4Rows + warp * 32;
+      const int n_warp = (kPair ? 2 * tile.n_tile + static_cast<int>(rank) : tile.n_tile) * kMx4Rows + quarter * 32;
       uint16_t* const y = p.y + static_cast<int64_t>(tile.row0) * p.ldy;
       if (split) break;  // finished below, with the other CTAs of the cluster
+      if constexpr (kPair) {
+        // Each set of warps takes every other 32 rows, rounds them into registers and
+        // gives the accumulator back before its first store: the odd CTA's release at
+        // cluster scope waits for the stores in front of it, 1.2 us a tile. Both
+        // together: 51200x5120 at 8192 rows 928 -> 900 us, 32 experts 5120x2560 at
+        // 32768 rows 272 -> 248; either alone gains nothing, the early release with
+        // one set of warps costs 15 % there (310 us).
+        uint32_t pairs[kMx4PairRows / 4], next[32];
+        const int first = warp >= 8 ? 32 : 0;
+        if (first < tile.rows) ptx::tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(first), next);
+#pragma unroll
+        for (int c = 0; c < kMx4PairRows; c += 64) {
+          const int c0 = c + first;
+          if (c0 >= tile.rows) break;
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            pairs[c / 4 + i] = bf16x2(__uint_as_float(next[2 * i]), __uint_as_float(next[2 * i + 1]));
+          if (c0 + 64 < tile.rows) ptx::tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c0 + 64), next);
+        }
+        ptx::tc_fence_before();
+        if (rank == 1) {
+          ptx::named_bar_sync(1, kEpilogueThreads);
+          if (threadIdx.x == 0)
+            ptx::mbar_arrive_remote_release(ptx::mapa(ptx::smem_addr(&bars->acc_empty[acc]), 0u));
+        } else {
+          ptx::mbar_arrive(ptx::smem_addr(&bars->acc_empty[acc]));
+        }
+#pragma unroll
+        for (int c = 0; c < kMx4PairRows; c += 64) {
+          const int c0 = c + first;
+          if (c0 >= tile.rows) break;
+          if (tile.rows - c0 <= 8)
+            store_pairs<1>(pairs + c / 4, lane, y, p.ldy, c0, tile.rows, n_warp, p.N);
+          else
+            store_pairs<4>(pairs + c / 4, lane, y, p.ldy, c0, tile.rows, n_warp, p.N);
+        }
+        continue;
+      }
       // The next 32 rows are read while the ones before are stored.
       uint32_t v[32], next[32];
       ptx::tmem_ld_32x32b_x32(taddr, next);
@@ -637,13 +692,7 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
           store_rows<4>(a, lane, y, p.ldy, c0, tile.rows, n_warp, p.N);
       }
       ptx::tc_fence_before();
-      if (kPair && rank == 1) {
-        ptx::named_bar_sync(1, 128);
-        if (threadIdx.x == 0)
-          ptx::mbar_arrive_remote_release(ptx::mapa(ptx::smem_addr(&bars->acc_empty[acc]), 0u));
-      } else {
-        ptx::mbar_arrive(ptx::smem_addr(&bars->acc_empty[acc]));
-      }
+      ptx::mbar_arrive(ptx::smem_addr(&bars->acc_empty[acc]));
     }
   }
   __syncwarp();
@@ -757,9 +806,12 @@ __global__ void __launch_bounds__(kMx4Threads, kPair ? 1 : 2)
 // Pair mode's activation scales: for every row tile and block, the image warp 9
 // makes of them in the other mode, so that the pair needs no generic write to
 // shared memory that the other CTA's tensor instructions have to see (a release
-// at cluster scope took 0.8 us a block). One CTA a row tile and 16 blocks.
+// at cluster scope took 0.8 us a block). One CTA a row tile and four blocks, all
+// of its reads in flight at once: with 16 blocks one after another it took 6.7 us in
+// front of 1024 rows of K = 5120 and 16 us in front of K = 27648.
 constexpr int kTileThreads = 256;
-constexpr int kTileBlocks = 16;
+constexpr int kTilePasses = 2;
+constexpr int kTileBlocks = 2 * kTilePasses;
 
 __global__ void __launch_bounds__(kTileThreads)
     mx4_scale_tiles_kernel(const uint32_t* __restrict__ xs, const int32_t* __restrict__ offsets, int E, int T, int npad,
@@ -788,15 +840,24 @@ __global__ void __launch_bounds__(kTileThreads)
     }
   }
   __syncthreads();
-  const int row0 = found[0], rows = found[1], r = threadIdx.x;
+  const int row0 = found[0], rows = found[1];
   if (rows == 0) return;  // past the last row tile
-  uint32_t* dst = out + (static_cast<size_t>(rt) * kblocks + kb0) * (kMx4XsTileBytes / 4) + (r >> 7) * 128 +
-                  (r & 31) * 4 + ((r >> 5) & 3);
-#pragma unroll 4
-  for (int i = 0; i < 2 * kTileBlocks; ++i) {
-    const int g = 2 * kb0 + i;
-    if (g >= 2 * kblocks) break;
-    dst[i * 256] = r < rows && g < groups ? __ldg(xs + static_cast<size_t>(g) * T + row0 + r) : 0u;
+  // A thread: four rows 32 apart of one column group, 16 bytes of the image.
+  const int lane = threadIdx.x & 31, half = threadIdx.x >> 5 & 1;  // of 128 rows each
+  const int r0 = half * 128 + lane;
+  uint32_t v[kTilePasses][4];
+#pragma unroll
+  for (int i = 0; i < kTilePasses; ++i) {
+    const int g = 2 * kb0 + 4 * i + (threadIdx.x >> 6);
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      v[i][w] = r0 + 32 * w < rows && g < groups ? __ldg(xs + static_cast<size_t>(g) * T + row0 + r0 + 32 * w) : 0u;
+  }
+  uint4* dst = reinterpret_cast<uint4*>(out) + static_cast<size_t>(rt) * kblocks * (kMx4XsTileBytes / 16) + half * 32 + lane;
+#pragma unroll
+  for (int i = 0; i < kTilePasses; ++i) {
+    const int g = 2 * kb0 + 4 * i + (threadIdx.x >> 6);
+    if (g < 2 * kblocks) dst[static_cast<size_t>(g) * 64] = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
   }
 }
 
@@ -858,8 +919,11 @@ cudaError_t launch_mx4_gemm(const Mx4GemmMaps& maps, const Mx4GemmParams& p, int
   const cudaError_t st = allow_smem();
   if (st != cudaSuccess) return st;
   cudaLaunchAttribute attr[3];
-  const cudaLaunchConfig_t cfg = gemm_config(grid, p.pair ? 2 : p.split, smem_bytes, stream, attr);
-  if (p.pair) return cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<true, 1>, maps, p);
+  cudaLaunchConfig_t cfg = gemm_config(grid, p.pair ? 2 : p.split, smem_bytes, stream, attr);
+  if (p.pair) {
+    cfg.blockDim = dim3(kMx4PairThreads);
+    return cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<true, 1>, maps, p);
+  }
   return p.bps == 2 ? cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<false, 2>, maps, p)
                     : cudaLaunchKernelEx(&cfg, spense_mx4_gemm_kernel<false, 1>, maps, p);
 }

@@ -55,6 +55,7 @@ struct Mx4GemmMaps {
 };
 
 constexpr int kMx4MaxTile = 240;  // rows a tile takes: with three words in front, one box of 256 scale words
+constexpr int kMx4PairRows = 256;  // the same of a pair, the most an MMA takes
 
 struct Mx4GemmPlan {
   int npad, stages, nacc, bps, pair, split, ctas_per_sm, grid;
