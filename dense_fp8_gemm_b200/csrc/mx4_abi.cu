@@ -66,23 +66,47 @@ double mx4_cost(int n, int split, int cps, int64_t tiles, int kblocks, double we
 // Few tiles: clusters of up to 8 CTAs split K, when the device holds all of them
 // at once and their partials fit the ring.
 //
-// Pairs (256 weight rows and up to 192 activation rows by two SMs, as many as leave
-// tensor memory for two accumulators and five stages' scales) read a third fewer
-// bytes from L2 for the same products, but a launch in front orders their scales
-// and both CTAs fill before the first product. They pay from 4e11 flops on: 51200x5120
-// at 1024, 2048 and 4096 rows 126 -> 126, 272 -> 223 and 535 -> 425 us, 5120x27648 at
-// 2048 rows 129 -> 119 us, 10240x5120 at 2048 rows 57 -> 59 us. Experts also need 512
-// rows on average (8 x 5120x5120 at 2048 rows each 209 -> 188 us, 128 x 2560x2048 at
-// 256 rows each 132 -> 144 us) and all of them ten blocks of K (16 x 4096x1408: 145 ->
-// 158 us).
+// Pairs: 256 weight rows and up to 256 activation rows by two SMs. They read up to a
+// third fewer bytes from L2 for the same products, but a launch in front orders their
+// scales and both CTAs fill before the first product. Dense products take whichever
+// mx4_cost and mx4_pair_cost call cheaper (singles against pairs: 51200x5120 at 128,
+// 256 and 1024 rows 27 -> 28, 52 -> 36 and 149 -> 120 us, 5120x5120 at 1024 and 4096
+// rows 19.5 -> 18.6 and 64 -> 51, 8192x1408 at 2048 rows 31 -> 25, 8192x256 at 16384
+// rows 117 -> 107). With experts pairs take 256 rows a tile from 256 rows on average
+// and 5e10 flops on (128 x 2560x2048 at 256 rows each 166 -> 144 us, 4 x 10240x5120 at
+// 256 rows 48 -> 42, 8 x 8192x512 at 1024 rows 68 -> 67), and 192, which leaves tensor
+// memory for two accumulators, from 128 rows and 1e11 flops on (128 x 2560x2048 at 128
+// rows 101 -> 94 us, at 64 rows 76 -> 78; 8 x 5120x5120 at 128 rows 32 -> 33).
+constexpr int kMx4PairLeast = 128;  // rows, of an expert on average
+constexpr int kMx4PairMore = 3;     // row tiles tried beyond the fewest
+
+// A wave of pair tiles takes 0.19 us + 0.55 ns a row for every block and 0.3 us + 6 ns a
+// row beside them, 5 us go before and after: fitted to 15 shapes (M 512 .. 4096) in
+// tiles of 96 to 256 rows, of which it finds the fastest or one within 5 %.
+double mx4_pair_cost(int n, int64_t tiles, int kblocks, double weight_bytes, int sms) {
+  const double waves = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2));
+  const double t = 5.0 + waves * (kblocks * (0.19 + 0.00055 * n) + 0.3 + 0.006 * n);
+  return std::max(t, 5.0 + weight_bytes / 5.5e6) + 0.05 * t;
+}
+
+bool mx4_experts_in_pairs(int64_t E, int64_t T, double flops) {
+  return T >= kMx4PairLeast * E && flops * std::min<int64_t>(T / E, 256) >= 1.28e13;
+}
+
+// The row tiles of pairs at most for T rows or fewer.
+int64_t mx4_pair_tiles(int64_t E, int64_t T, bool ragged) {
+  if (T < kMx4PairLeast * (ragged ? E : 1)) return 0;
+  return ragged ? E + T / kMx4PairLeast : (T + kMx4PairRows - 1) / kMx4PairRows + kMx4PairMore;
+}
+
 spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, Mx4GemmPlan* out) {
   Mx4GemmPlan pl{};
   const uint32_t tail = static_cast<uint32_t>(round_up(kMx4BarrierBytes + 4 * (3 * static_cast<size_t>(E) + 1), 16));
   const int64_t active = ragged ? std::min(E, T) : 1;
   const double flops = 2.0 * T * n_tiles * kMx4Rows * kblocks * kMx4Cols;
   const int64_t avg = (T + E - 1) / E;
-  pl.pair = flops >= 4e11 && kblocks >= 10 && (!ragged || avg >= 512) ? 1 : 0;
-  const int most = pl.pair ? kMx4PairRows : kMx4MaxTile, step = pl.pair ? 32 : 16;
+  pl.pair = ragged && mx4_experts_in_pairs(E, T, flops) ? 1 : 0;
+  const int step = pl.pair ? 32 : 16;
   // Row tiles at most: every expert's last one may be short.
   auto row_tiles = [&](int n) { return ragged ? active + T / n : (T + n - 1) / n; };
   auto stage = [&](int n) {
@@ -95,12 +119,13 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
   };
   pl.split = pl.ctas_per_sm = 1;
   const double weight_bytes = static_cast<double>(active) * n_tiles * kblocks * kMx4BlockBytes;
-  const int64_t m0 = ragged ? 1 : (T + most - 1) / most;
+  const int64_t m0 = ragged ? 1 : (T + kMx4MaxTile - 1) / kMx4MaxTile;
   double best = 0.0;
-  for (int64_t m = m0; m < m0 + (ragged || pl.pair ? 1 : 16); ++m) {
+  for (int64_t m = m0; m < m0 + (ragged ? 1 : 16); ++m) {
     int n;
     if (ragged)
-      n = pl.pair ? most : static_cast<int>(std::min<int64_t>(round_up(std::max<int64_t>(2 * avg, 32), 16), 208));
+      n = pl.pair ? (avg >= 256 ? kMx4PairRows : 192)
+                  : static_cast<int>(std::min<int64_t>(round_up(std::max<int64_t>(2 * avg, 32), 16), 208));
     else
       n = static_cast<int>(round_up((T + m - 1) / m, step));
     n = static_cast<int>(std::min<int64_t>(n, round_up(T, step)));
@@ -121,6 +146,21 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
       }
     }
     if (n <= step) break;
+  }
+  if (!ragged && T >= kMx4PairLeast) {
+    // A CTA's later tiles also wait for the epilogues of the ones before.
+    const int64_t singles = row_tiles(pl.npad) * n_tiles;
+    if (pl.split == 1) best += 0.01 * pl.npad * static_cast<double>((singles + sms - 1) / sms - 1);
+    const int64_t p0 = (T + kMx4PairRows - 1) / kMx4PairRows;
+    for (int64_t m = p0; m <= p0 + kMx4PairMore; ++m) {
+      const int n = static_cast<int>(round_up((T + m - 1) / m, 32));
+      const double c = mx4_pair_cost(n, row_tiles(n) * ((n_tiles + 1) / 2), kblocks, weight_bytes, sms);
+      if (c < best) {
+        best = c;
+        pl.pair = pl.split = pl.ctas_per_sm = 1;
+        pl.npad = n;
+      }
+    }
   }
   pl.row_tiles = row_tiles(pl.npad);
   const int64_t tiles = pl.row_tiles * (pl.pair ? (n_tiles + 1) / 2 : n_tiles);
@@ -429,18 +469,11 @@ size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M) {
     fail(SPENSE_ERR_ARG, "Wp is NULL or M outside [0, 2^20]");
     return 0;
   }
-  if (M == 0) return kMx4Header;
-  int dev = 0;
-  DeviceInfo info;
-  if (current_device(&dev, &info) != SPENSE_OK) return 0;
   // A weight of one expert serves both products, which may be planned differently.
-  size_t bytes = 0;
-  for (int ragged = Wp->E > 1 ? 1 : 0; ragged < 2; ++ragged) {
-    Mx4GemmPlan pl;
-    if (make_mx4_plan(Wp->E, Wp->n_tiles, Wp->kblocks, M, ragged != 0, info.sms, &pl) != SPENSE_OK) return 0;
-    bytes = std::max(bytes, pl.workspace_bytes);
-  }
-  return bytes;
+  // Enough for fewer rows too, whose tiles may be more.
+  int64_t tiles = mx4_pair_tiles(Wp->E, M, true);
+  if (Wp->E == 1) tiles = std::max(tiles, mx4_pair_tiles(1, M, false));
+  return kMx4Header + static_cast<size_t>(tiles) * Wp->kblocks * kMx4XsTileBytes;
 }
 
 spense_status spense_mx4_gemm(const spense_mx4_packed* Wp, const uint8_t* Xq, const uint8_t* x_scale, int64_t M,

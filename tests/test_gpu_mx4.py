@@ -357,6 +357,79 @@ def test_gemm_experts_large_enough_for_pairs(counts, spare):
     pw.free()
 
 
+def values_on_device(q, s):
+    """ref.values in float64 on the device."""
+    lut = torch.from_numpy(np.concatenate((ref.LEVELS, -ref.LEVELS))).to(q.device, torch.float64)
+    v = lut[torch.stack((q & 15, q >> 4), -1).long()].view(*s.shape, 32)
+    return (v * torch.exp2(s.double() - 127.0)[..., None]).view(s.shape[0], -1)
+
+
+def check_all(y, xq, xs, wq, ws):
+    """Every element of y against ref.gemm's value and tolerance, computed in float64 on the device."""
+    x = values_on_device(xq, xs)
+    terms = -(-x.shape[1] // 64) + 8
+    for n in range(0, wq.shape[0], 4096):
+        w = values_on_device(wq[n:n + 4096], ws[n:n + 4096])
+        want, acc = x @ w.T, x.abs() @ w.abs().T * (terms * 2.0 ** -23)
+        bad = (y[:, n:n + 4096].double() - want).abs() > (want.abs() + acc) * 2.0 ** -8 + acc + 2.0 ** -134
+        assert not bool(bad.any()), (n, bad.nonzero()[:4])
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (129, 25601, 2720), (161, 25728, 1184), (200, 25600, 2592), (256, 25600, 2592), (257, 25601, 2592),
+    (385, 25600, 1056), (513, 19000, 1056), (700, 19000, 1056), (1024, 5120, 5120), (1100, 4000, 5120),
+    (16384, 8192, 160), (8193, 9001, 288), (1500, 10112, 1312), (16000, 2001, 544)])
+def test_gemm_tiles_of_pairs(M, N, K):
+    """Pair tiles of 160 to 256 rows, full and short, one and several a CTA, over one block of K and more."""
+    wq, ws = device_operands(M, N, K)
+    xq, xs = device_operands(N, M, K)
+    pw = spense.mx4_pack(wq, ws)
+    wsp = spense.new_workspace(spense.mx4_workspace_size(pw, M))
+    y = spense.mx4_gemm(pw, xq, words_of(xs), workspace=wsp)
+    again = spense.mx4_gemm(pw, xq, words_of(xs), workspace=wsp)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    assert spense.workspace_status(wsp) == 0
+    check_all(y, xq, xs, wq, ws)
+    pw.free()
+
+
+@pytest.mark.parametrize("N,counts,spare", [
+    (20480, [599, 1], 0), (20470, [0, 470, 170], 5), (9000, [0, 256, 257, 255, 1000], 1),
+    (8320, [135 + 7 * (i % 5) * (-1) ** i for i in range(20)], 2), (8320, [0, 2700] + [0] * 17 + [192], 0)])
+def test_gemm_experts_tiles_of_pairs(N, counts, spare):
+    E, T, K = len(counts), sum(counts) + spare, 2592
+    wq, ws = device_operands(1, E * N, K)
+    xq, xs = device_operands(2, T, K)
+    pw = spense.mx4_pack(wq.view(E, N, -1), ws.view(E, N, -1))
+    off = offsets_of(counts)
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    wsp = spense.new_workspace(spense.mx4_workspace_size(pw, T))
+    spense.mx4_gemm_experts(pw, xq, words_of(xs), torch.from_numpy(off).cuda(), Y=y, workspace=wsp)
+    assert spense.workspace_status(wsp) == 0
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        if b > a:
+            check_all(y[a:b], xq[a:b], xs[a:b], wq[e * N:(e + 1) * N], ws[e * N:(e + 1) * N])
+    assert bool((y[off[-1]:] == 7).all())
+    pw.free()
+
+
+def test_workspace_serves_fewer_rows():
+    """One sized for M rows is enough for every smaller M, whose tiles may be more."""
+    N, K = 5120, 1056
+    wq, ws = device_operands(3, N, K)
+    pw = spense.mx4_pack(wq, ws)
+    sizes = [spense.mx4_workspace_size(pw, M) for M in range(2049)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    for top in (128, 700, 1025, 2048):
+        wsp = spense.new_workspace(sizes[top])
+        for M in (1, top // 3, top // 2 + 1, top - 1, top):
+            xq, xs = device_operands(M, M, K)
+            y = spense.mx4_gemm(pw, xq, words_of(xs), workspace=wsp)
+            check_all(y, xq, xs, wq, ws)
+    pw.free()
+
+
 def test_small_workspace_is_refused():
     q, s, pw = packed(13, 1, 256, 512)
     _, _, xqd, xsd = activations(14, 5, 512)
