@@ -48,7 +48,8 @@ int clusters_at_once(int s, int cps, int sms) {
 // 1024) x tiles x splits the choices by it are within 20 % of the best.
 double mx4_cost(int n, int split, int cps, int64_t tiles, int kblocks, double weight_bytes, int sms) {
   const int64_t ctas = tiles * split;
-  const double blocks = split == 1 ? static_cast<double>((tiles + sms - 1) / sms) * kblocks : (kblocks + split - 1) / split;
+  const double waves = static_cast<double>((tiles + sms - 1) / sms);
+  const double blocks = split == 1 ? waves * kblocks : (kblocks + split - 1) / split;
   const double l2 = (kMx4BlockBytes + n * 136.0) * static_cast<double>(std::min<int64_t>(ctas, sms)) / 12.4e6;
   const double block = std::max(0.27 + 0.0006 * n, l2) * (cps == 2 ? 1.5 : 1.0);
   const double t = 3.2 + 0.006 * n + blocks * block + (split > 1 ? 0.8 + 0.012 * n : 0.0);
@@ -265,8 +266,8 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(h->K / 2)};
     const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(p.box[i])};
     const cuuint32_t estr[2] = {1u, 1u};
-    const CUresult r = encode(&maps.x[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(Xq), dims, strides, box,
-                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const CUresult r = encode(&maps.x[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(Xq), dims, strides,
+                              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(SPENSE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }

@@ -32,15 +32,15 @@
 // (cta_group::2), each with its own 128 weight rows and half of the activation rows,
 // which cuts the bytes a flop moves into shared memory by a third. All copies of a
 // pair are counted on the even CTA's barriers; the scales come in the tensor core's
-// order from a launch in front. Warps 8-11 are a second set of epilogue warps: a
-// tile's MMAs of 10 blocks take as long as one set needs for its 192 rows.
+// order from a launch in front. Warps 8-11 are a second set of epilogue warps.
 //
 // Bound: up to some 250 rows by the weights' way from HBM (0.53 bytes an element:
 // 64 experts 2560x5120 at 32 rows 36.2 us, 0.88 of the measured copy rate; 128
 // experts 2560x2048 at 509 rows 59.3 us, 0.92), for few weights by the 3.2 us around
 // the blocks and a CTA's 0.25 us a block (10240x5120 at one row 7.5 us), beyond by the
-// tensor pipe and the power cap (51200x5120 at 8192 rows 925 us, 4.6 PFLOP/s at a clock
-// of 1.17 GHz).
+// tensor pipe and the power cap (51200x5120 at 8192 rows 824 us, 5.2 PFLOP/s; 5120x5120
+// at 4096 rows 47 us, 4.6), for K of a few blocks by the L2 (20480x2560 at 16384 rows
+// 10.4 TB/s of tiles in and 1.7 of Y out).
 //
 // Every wait is bounded (1.5 s); on expiry the kernel records a code in the
 // workspace's status word and all roles leave their loops.
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(kPair ? kMx4PairThreads : kMx4Threads, kPair ?
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(ptx::smem_addr(&bars->acc_full[a]), 1);
-      // pair mode: the odd CTA's epilogue arrives once, remotely
-      ptx::mbar_init(ptx::smem_addr(&bars->acc_empty[a]), kPair ? 257 : 128);
+      // pair mode: eight warps of each CTA arrive on the even CTA's
+      ptx::mbar_init(ptx::smem_addr(&bars->acc_empty[a]), kPair ? 16 : 128);
     }
     bars->abort_flag = 0;
     ptx::fence_mbar_init();
@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(kPair ? kMx4PairThreads : kMx4Threads, kPair ?
             ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(nb) * bytes);
 #pragma unroll
             for (int j = 0; j < kBlocks; ++j)
-              if (j < nb) ptx::tma_load_2d(dst + static_cast<uint32_t>(j * p.npad) * 128u, map, (kb + j) * 128, row0, full, pol);
+              if (j < nb)
+                ptx::tma_load_2d(dst + static_cast<uint32_t>(j * p.npad) * 128u, map, (kb + j) * 128, row0, full, pol);
           }
         }
       }
@@ -638,11 +639,12 @@ __global__ void __launch_bounds__(kPair ? kMx4PairThreads : kMx4Threads, kPair ?
       if (split) break;  // finished below, with the other CTAs of the cluster
       if constexpr (kPair) {
         // Each set of warps takes every other 32 rows, rounds them into registers and
-        // gives the accumulator back before its first store: the odd CTA's release at
-        // cluster scope waits for the stores in front of it, 1.2 us a tile. Both
-        // together: 51200x5120 at 8192 rows 928 -> 900 us, 32 experts 5120x2560 at
-        // 32768 rows 272 -> 248; either alone gains nothing, the early release with
-        // one set of warps costs 15 % there (310 us).
+        // gives the accumulator back before its first store: 32 experts 5120x2560 at
+        // 32768 rows 272 -> 248 us, where one set of warps gains nothing without and
+        // loses with it (310 us). The signal carries no memory access, the reads of
+        // tensor memory are complete (wait, fence): relaxed, since a release at cluster
+        // scope takes 0.6 us with the accumulator idle (51200x5120 at 8192 rows 906 ->
+        // 824 us, at the power cap).
         uint32_t pairs[kMx4PairRows / 4], next[32];
         const int first = warp >= 8 ? 32 : 0;
         if (first < tile.rows) ptx::tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(first), next);
@@ -657,13 +659,8 @@ __global__ void __launch_bounds__(kPair ? kMx4PairThreads : kMx4Threads, kPair ?
           if (c0 + 64 < tile.rows) ptx::tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c0 + 64), next);
         }
         ptx::tc_fence_before();
-        if (rank == 1) {
-          ptx::named_bar_sync(1, kEpilogueThreads);
-          if (threadIdx.x == 0)
-            ptx::mbar_arrive_remote_release(ptx::mapa(ptx::smem_addr(&bars->acc_empty[acc]), 0u));
-        } else {
-          ptx::mbar_arrive(ptx::smem_addr(&bars->acc_empty[acc]));
-        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_remote_relaxed(ptx::mapa(ptx::smem_addr(&bars->acc_empty[acc]), 0u));
 #pragma unroll
         for (int c = 0; c < kMx4PairRows; c += 64) {
           const int c0 = c + first;
@@ -853,7 +850,8 @@ __global__ void __launch_bounds__(kTileThreads)
     for (int w = 0; w < 4; ++w)
       v[i][w] = r0 + 32 * w < rows && g < groups ? __ldg(xs + static_cast<size_t>(g) * T + row0 + r0 + 32 * w) : 0u;
   }
-  uint4* dst = reinterpret_cast<uint4*>(out) + static_cast<size_t>(rt) * kblocks * (kMx4XsTileBytes / 16) + half * 32 + lane;
+  uint4* dst =
+      reinterpret_cast<uint4*>(out) + static_cast<size_t>(rt) * kblocks * (kMx4XsTileBytes / 16) + half * 32 + lane;
 #pragma unroll
   for (int i = 0; i < kTilePasses; ++i) {
     const int g = 2 * kb0 + 4 * i + (threadIdx.x >> 6);
