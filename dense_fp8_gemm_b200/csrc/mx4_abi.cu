@@ -320,11 +320,10 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
   p.last_steps = (tail_cols + 63) / 64;
   p.npad = pl.npad;
   // Activation codes of up to 32 MB stay in L2 while all weights pass, and the weights
-  // are read once (51200x5120 at 8192 rows 998 us, in groups of 12 row tiles 1042 us, at
-  // the power cap). More of them go in groups of 16 row tiles: 20480x5120 at 65536 rows
-  // 3490 -> 3130 us, 5120x27648 at 16384 rows 1223 -> 1033 us, 5120x5120 at 32768 rows 438
-  // -> 400 us.
-  p.group = T * (h->K / 2) <= (32 << 20) ? 1 << 16 : 16;
+  // are read once. More of them go in groups of 24 row tiles: 5120x27648 at 16384 rows
+  // 1051 -> 901 us (in groups of 12 950, of 32 953), 20480x5120 at 32768 rows 1377 ->
+  // 1350 (of 12 1527, of 16 1383).
+  p.group = T * (h->K / 2) <= (32 << 20) ? 1 << 16 : 24;
   p.stages = pl.stages;
   p.nacc = pl.nacc;
   p.bps = pl.bps;
