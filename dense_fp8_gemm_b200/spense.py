@@ -725,6 +725,8 @@ def mx4_pack(Wq: torch.Tensor, w_scale: torch.Tensor, stream=None) -> Mx4Weight:
 
 
 def mx4_workspace_size(pw: Mx4Weight, M: int) -> int:
+    """spense_mx4_workspace_size: bytes for M rows or fewer. The workspace is the
+    MXFP4 products' own: they do not leave it zero, as the FP8 products need it."""
     n = lib().spense_mx4_workspace_size(pw.handle, M)
     if n == 0:
         _check(1, "spense_mx4_workspace_size")

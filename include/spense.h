@@ -528,7 +528,7 @@ typedef struct spense_mx4_info {
 
 SPENSE_API spense_status spense_mx4_get_info(const spense_mx4_packed* Wp, spense_mx4_info* info);
 
-/* Bytes of workspace the MXFP4 products need for M rows; 0 on a bad argument. */
+/* Bytes of workspace the MXFP4 products need for M rows or fewer; 0 on a bad argument. */
 SPENSE_API size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M);
 
 /*
@@ -542,7 +542,10 @@ SPENSE_API size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t
  *   Y            device, bf16, row m at Y + m * ldy, N <= ldy <= 2^30, 16-byte
  *                aligned (16-byte stores are used when ldy % 8 == 0).
  *   workspace    at least spense_mx4_workspace_size bytes, 256-byte aligned,
- *                ZERO-FILLED before its first use, with the rules of spense_gemm;
+ *                ZERO-FILLED before its first use. It serves any number of MXFP4
+ *                products issued in stream order (not concurrently, in captured
+ *                graphs either). What lies behind its first 256 bytes does not stay
+ *                zero: zero it again before spense_gemm or its kin take it.
  *                spense_workspace_status reads its status word.
  * Asynchronous on `stream`. Errors: ARG, SHAPE, ALIGN, WORKSPACE, UNSUPPORTED, CUDA.
  */
