@@ -430,6 +430,46 @@ def test_workspace_serves_fewer_rows():
     pw.free()
 
 
+def test_pairs_on_two_streams_and_captured():
+    """Two products in pairs and a small one, on two streams at once, and each stream's sequence as a graph."""
+    sets = []
+    for i, (M, N, K) in enumerate(((1024, 5120, 5120), (300, 25600, 2592), (5, 640, 1056))):
+        wq, ws = device_operands(40 + i, N, K)
+        xq, xs = device_operands(50 + i, M, K)
+        pw = spense.mx4_pack(wq, ws)
+        y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+        wsp = spense.new_workspace(spense.mx4_workspace_size(pw, M))
+        sets.append((spense.PreparedMx4Gemm(pw, xq, words_of(xs), y, wsp), y, wsp, (xq, xs, wq, ws)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    order = [[0, 2, 0], [1, 1]]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, todo in zip(streams, order):
+            for i in todo:
+                sets[i][0](st)
+    torch.cuda.synchronize()
+    for call, y, wsp, operands in sets:
+        check_all(y, *operands)
+        assert spense.workspace_status(wsp) == 0
+        y.zero_()
+    graphs = []
+    for st, todo in zip(streams, order):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for i in todo:
+                sets[i][0]()
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for call, y, wsp, operands in sets:
+        check_all(y, *operands)
+        assert spense.workspace_status(wsp) == 0
+
+
 def test_small_workspace_is_refused():
     q, s, pw = packed(13, 1, 256, 512)
     _, _, xqd, xsd = activations(14, 5, 512)
