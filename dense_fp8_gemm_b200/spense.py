@@ -3,10 +3,15 @@ only. Every step of the GEMM path runs in the CUDA library ``libspense.so``;
 there is no CPU or PyTorch fallback — if the library cannot be loaded or no
 sm_100 device is present, calls raise.
 
-PyTorch supplies device memory and streams; tensors are passed by address.
+PyTorch supplies device memory and streams; tensors are passed by address. What
+an MXFP4 or expert call is not given it makes on the stream it runs on (`stream`, or
+torch's current one). Tensors given to a call on another stream than their own
+follow torch's rules: the caller orders the two streams, and keeps the tensors (or
+record_stream's them) until the work there is done.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -600,6 +605,13 @@ def _raw(stream, dev: int) -> int:
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
+def _made_on(stream):
+    """Where a call makes the buffers that it was not given: on the stream it launches
+    on. Made on another one, their memory (and a workspace's zero fill) would be
+    ordered by that one's work, before the call and once they are dropped."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _scale_flags(x_scale: torch.Tensor, M: int, K: int) -> int:
     """MX4_SCALE_ROWS for scales [M, K / 32], 0 for words [ceil(K / 128), M, 4]."""
     if x_scale.shape == (-(-K // 128), M, 4):
@@ -627,12 +639,14 @@ def mx4_quantize(X: torch.Tensor, rows: torch.Tensor | None = None, scale_rows: 
     x, ldx = _rows_addr(X, dtype, dev, "X", M, K)
     T, r = (M, None) if rows is None else (rows.shape[0], _addr(rows, torch.int32, dev, "rows"))
     if Xq is None:
-        Xq = torch.empty(T, K // 2, dtype=torch.uint8, device=X.device)
+        with _made_on(stream):
+            Xq = torch.empty(T, K // 2, dtype=torch.uint8, device=X.device)
     elif Xq.shape != (T, K // 2):
         raise ValueError(f"Xq must be [{T}, {K // 2}], got {tuple(Xq.shape)}")
     if x_scale is None:
-        x_scale = torch.empty(*((T, K // 32) if scale_rows else (-(-K // 128), T, 4)), dtype=torch.uint8,
-                              device=X.device)
+        with _made_on(stream):
+            x_scale = torch.empty(*((T, K // 32) if scale_rows else (-(-K // 128), T, 4)), dtype=torch.uint8,
+                                  device=X.device)
     elif scale_rows and x_scale.shape != (T, K // 32):
         raise ValueError(f"x_scale must be [{T}, {K // 32}], got {tuple(x_scale.shape)}")
     flags = MX4_SCALE_ROWS if scale_rows else _scale_flags(x_scale, T, K)
@@ -653,7 +667,8 @@ def mx4_dequantize(Xq: torch.Tensor, x_scale: torch.Tensor, dtype=torch.bfloat16
     M, K = Xq.shape
     K *= 2
     if out is None:
-        out = torch.empty(M, K, dtype=dtype, device=Xq.device)
+        with _made_on(stream):
+            out = torch.empty(M, K, dtype=dtype, device=Xq.device)
     if out.shape != (M, K) or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"the output must be bfloat16 or float32 [{M}, {K}], got {out.dtype} {tuple(out.shape)}")
     code = lib().spense_mx4_dequantize(_addr(Xq, torch.uint8, dev, "Xq"), _addr(x_scale, torch.uint8, dev, "x_scale"),
@@ -772,10 +787,12 @@ def mx4_gemm(pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, Y: torch.Te
              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """spense_mx4_gemm: Y [M, N] bf16 = X x W^T of MXFP4 activations (mx4_quantize) and
     a packed weight. Y may be a column slice of a wider tensor."""
-    if Y is None:
-        Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
-    if workspace is None:
-        workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
+    if Y is None or workspace is None:
+        with _made_on(stream):
+            if Y is None:
+                Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
+            if workspace is None:
+                workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
     PreparedMx4Gemm(pw, Xq, x_scale, Y, workspace)(stream)
     return Y
 
@@ -785,10 +802,12 @@ def mx4_gemm_experts(pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, off
     """spense_mx4_gemm_experts: rows offsets[e] .. offsets[e + 1] (device int32
     [E + 1]) of X with expert e's weight. Rows outside every range are left as
     they were in Y (unset in a Y made here)."""
-    if Y is None:
-        Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
-    if workspace is None:
-        workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
+    if Y is None or workspace is None:
+        with _made_on(stream):
+            if Y is None:
+                Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
+            if workspace is None:
+                workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
     PreparedMx4Gemm(pw, Xq, x_scale, Y, workspace, offsets)(stream)
     return Y
 
@@ -815,7 +834,8 @@ def expert_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, 
         need = _sort_workspace(M, k, E) // 4
         if need == 0:
             _check(2, "spense_expert_sort")
-        made = torch.empty(need + 2 * n + E + 1, dtype=torch.int32, device=ids.device)
+        with _made_on(stream):
+            made = torch.empty(need + 2 * n + E + 1, dtype=torch.int32, device=ids.device)
         ws, r, p, o = made.split_with_sizes((need, n, n, E + 1))
         workspace = ws if workspace is None else workspace
         rows = r if rows is None else rows
@@ -846,7 +866,8 @@ def expert_combine(Y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, ou
     M, k = pos.shape
     y, ldy = _rows_addr(Y, torch.bfloat16, dev, "Y", T, N)
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=Y.device)
+        with _made_on(stream):
+            out = torch.empty(M, N, dtype=torch.bfloat16, device=Y.device)
     elif out.shape != (M, N):
         raise ValueError(f"out must be [{M}, {N}], got {tuple(out.shape)}")
     o, ldo = _rows_addr(out, torch.bfloat16, dev, "out", M, N)
