@@ -4,10 +4,10 @@ there is no CPU or PyTorch fallback — if the library cannot be loaded or no
 sm_100 device is present, calls raise.
 
 PyTorch supplies device memory and streams; tensors are passed by address. What
-an MXFP4 or expert call is not given it makes on the stream it runs on (`stream`, or
-torch's current one). Tensors given to a call on another stream than their own
-follow torch's rules: the caller orders the two streams, and keeps the tensors (or
-record_stream's them) until the work there is done.
+a call is not given it makes on the stream it runs on (`stream`, or torch's current
+one). Tensors given to a call on another stream than their own follow torch's rules:
+the caller orders the two streams, and keeps the tensors (or record_stream's them)
+until the work there is done.
 """
 from __future__ import annotations
 
@@ -307,14 +307,23 @@ def new_workspace(nbytes: int, device=None) -> torch.Tensor:
     return torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
 
 
+def _made_on(stream):
+    """Where a call makes the buffers that it was not given: on the stream it launches
+    on. Made on another one, their memory (and a workspace's zero fill) would be
+    ordered by that one's work, before the call and once they are dropped."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def gemm(pw: PackedWeight, X: torch.Tensor, x_scale: torch.Tensor, Y: torch.Tensor | None = None,
          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """spense_gemm: Y [M, N] bf16 = X [M, K] e4m3 x packed W^T, scaled."""
     M = X.shape[0]
-    if Y is None:
-        Y = torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device)
-    if workspace is None:
-        workspace = new_workspace(workspace_size(pw, M), X.device)
+    if Y is None or workspace is None:
+        with _made_on(stream):
+            if Y is None:
+                Y = torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device)
+            if workspace is None:
+                workspace = new_workspace(workspace_size(pw, M), X.device)
     code = lib().spense_gemm(pw.handle, _dev_ptr(X, torch.uint8, "X"),
                              _dev_ptr(x_scale, torch.float32, "x_scale"), M,
                              _dev_ptr(Y, torch.bfloat16, "Y"), _dev_ptr(workspace, torch.uint8, "workspace"),
@@ -362,10 +371,12 @@ def gemm_grouped(pws, X: torch.Tensor, x_scale: torch.Tensor, Ys=None, workspace
     with Ys given as flat device tensors (views into a wider output). Returns
     the list of outputs."""
     M = X.shape[0]
-    if Ys is None:
-        Ys = [torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device) for pw in pws]
-    if workspace is None:
-        workspace = new_workspace(grouped_workspace_size(pws, M), X.device)
+    if Ys is None or workspace is None:
+        with _made_on(stream):
+            if Ys is None:
+                Ys = [torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device) for pw in pws]
+            if workspace is None:
+                workspace = new_workspace(grouped_workspace_size(pws, M), X.device)
     yarr = (ctypes.c_void_p * len(pws))()
     strided = any(not Y.is_contiguous() for Y in Ys)
     if strided and ldy is None:
@@ -476,10 +487,12 @@ def quantize(X: torch.Tensor, order: PackedWeight | None = None, Xq: torch.Tenso
     columns in `order`'s packed order when a packed weight is given. Returns
     (Xq uint8 [M, K], x_scale float32 [M])."""
     M, K = X.shape
-    if Xq is None:
-        Xq = torch.empty((M, K), dtype=torch.uint8, device=X.device)
-    if x_scale is None:
-        x_scale = torch.empty((M,), dtype=torch.float32, device=X.device)
+    if Xq is None or x_scale is None:
+        with _made_on(stream):
+            if Xq is None:
+                Xq = torch.empty((M, K), dtype=torch.uint8, device=X.device)
+            if x_scale is None:
+                x_scale = torch.empty((M,), dtype=torch.float32, device=X.device)
     code = lib().spense_quantize(_dev_ptr(X, torch.bfloat16, "X"), M, K, None if order is None else order.handle,
                                  _dev_ptr(Xq, torch.uint8, "Xq"), _dev_ptr(x_scale, torch.float32, "x_scale"),
                                  _stream(stream))
@@ -545,10 +558,12 @@ def score_glu(down: torch.Tensor, s_down: torch.Tensor, h_in: torch.Tensor, h_mi
     [H, I] (+ fp32 [H]); h_in [H], h_mid [I] fp32 Hessian diagonals. Returns
     score fp32 [I]."""
     H, I = down.shape
-    if score is None:
-        score = torch.empty((I,), dtype=torch.float32, device=down.device)
-    if workspace is None:
-        workspace = new_workspace(max(256, int(lib().spense_score_workspace_size(I, H))), down.device)
+    if score is None or workspace is None:
+        with _made_on(stream):
+            if score is None:
+                score = torch.empty((I,), dtype=torch.float32, device=down.device)
+            if workspace is None:
+                workspace = new_workspace(max(256, int(lib().spense_score_workspace_size(I, H))), down.device)
     code = lib().spense_score_glu(_dev_ptr(gate, torch.uint8, "gate"), _dev_ptr(s_gate, torch.float32, "s_gate"),
                                   _dev_ptr(up, torch.uint8, "up"), _dev_ptr(s_up, torch.float32, "s_up"), I, H,
                                   _dev_ptr(down, torch.uint8, "down"), _dev_ptr(s_down, torch.float32, "s_down"),
@@ -564,7 +579,8 @@ def select_dense(score: torch.Tensor, Kd: int, out: torch.Tensor | None = None, 
     ascending int32 indices on the device."""
     I = score.shape[0]
     if out is None:
-        out = torch.empty((Kd,), dtype=torch.int32, device=score.device)
+        with _made_on(stream):
+            out = torch.empty((Kd,), dtype=torch.int32, device=score.device)
     code = lib().spense_select_dense(_dev_ptr(score, torch.float32, "score"), I, int(Kd),
                                      _dev_ptr(out, torch.int32, "dense_idx") if Kd > 0 else None, _stream(stream))
     _check(code, "spense_select_dense")
@@ -603,13 +619,6 @@ def _rows_addr(t: torch.Tensor, dtype, dev: int, name: str, rows: int, cols: int
 
 def _raw(stream, dev: int) -> int:
     return _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-def _made_on(stream):
-    """Where a call makes the buffers that it was not given: on the stream it launches
-    on. Made on another one, their memory (and a workspace's zero fill) would be
-    ordered by that one's work, before the call and once they are dropped."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _scale_flags(x_scale: torch.Tensor, M: int, K: int) -> int:

@@ -119,3 +119,64 @@ def test_sort_keeps_its_counters_on_another_stream():
     assert all(bool((t == 7).all()) for t in later)
     for a, b in zip(into, want):
         assert torch.equal(a, b)
+
+
+def fp8_weight(N, K):
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    W = (torch.randn(N, K, device="cuda", generator=g)).to(torch.float8_e4m3fn).view(torch.uint8)
+    return W, torch.rand(N, device="cuda", generator=g) + 0.5
+
+
+def fp8_case(M, N, K):
+    X, s = fp8_weight(M, K)
+    return spense.pack(*fp8_weight(N, K), Kd=K // 4), X, s
+
+
+def fp8_quantise():
+    x = torch.randn(300, 1024, device="cuda").to(torch.bfloat16)
+    return lambda stream: spense.quantize(x, stream=stream)
+
+
+def fp8_product():
+    pw, X, s = fp8_case(40, 3000, 2048)
+    return lambda stream: (spense.gemm(pw, X, s, stream=stream),)
+
+
+def fp8_products_in_one_launch():
+    pws, X, s = [spense.pack(*fp8_weight(N, 2048), Kd=512) for N in (640, 1500)], *fp8_weight(33, 2048)
+    return lambda stream: spense.gemm_grouped(pws, X, s, stream=stream)
+
+
+def fp8_scores():
+    I, H = 1024, 512
+    gate, up, down = fp8_weight(I, H), fp8_weight(I, H), fp8_weight(H, I)
+    h_in, h_mid = torch.rand(H, device="cuda"), torch.rand(I, device="cuda")
+    return lambda stream: (spense.score_glu(*down, h_in, h_mid, *gate, *up, stream=stream),)
+
+
+def fp8_selection():
+    score = torch.rand(4096, device="cuda")
+    return lambda stream: (spense.select_dense(score, 1000, stream=stream),)
+
+
+@pytest.mark.parametrize("make", [fp8_quantise, fp8_product, fp8_products_in_one_launch, fp8_scores, fp8_selection])
+def test_fp8_outputs_made_on_another_stream(make):
+    after_the_past(make())
+
+
+def test_fp8_product_keeps_its_workspace_on_another_stream():
+    """Partials and counters of tiles that several CTAs share, in a workspace the call makes."""
+    pw, X, s = fp8_case(40, 51200, 2048)
+    y = torch.zeros(40, 51200, dtype=torch.bfloat16, device="cuda")
+    want = spense.gemm(pw, X, s)
+    n = spense.workspace_size(pw, 40)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    spense.gemm(pw, X, s, Y=y, stream=side)
+    later = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert not any(bool(t.any()) for t in later)
+    assert torch.equal(y.view(torch.int16), want.view(torch.int16))
