@@ -34,7 +34,10 @@ int clusters_at_once(int s, int cps, int sms) {
   if (cudaGetDevice(&dev) != cudaSuccess) return sms * cps / (s + 1);
   if (dev < kDevices && known[dev][s][cps] > 0) return known[dev][s][cps] - 1;
   int n = 0;
-  if (mx4_max_clusters(s, kMx4Smem[cps - 1], &n) != cudaSuccess) n = sms * cps / (s + 1);
+  if (mx4_max_clusters(s, kMx4Smem[cps - 1], &n) != cudaSuccess) {
+    cudaGetLastError();
+    return sms * cps / (s + 1);
+  }
   if (dev < kDevices) known[dev][s][cps] = n + 1;
   return n;
 }

@@ -57,7 +57,10 @@ spense_status ok() {
   return SPENSE_OK;
 }
 
+// The runtime keeps a thread's last error until it is asked for: a call that has
+// reported its own takes it along, or the next launch would report it again.
 spense_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
   if (e == cudaErrorMemoryAllocation)
     return fail(SPENSE_ERR_OOM, "%s: %s", what, cudaGetErrorString(e));
   return fail(SPENSE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -68,7 +71,10 @@ spense_status current_device(int* dev, DeviceInfo* info) {
   static std::mutex mu;
   static std::vector<DeviceInfo> cache;
   cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return fail(SPENSE_ERR_UNSUPPORTED, "no CUDA device: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(SPENSE_ERR_UNSUPPORTED, "no CUDA device: %s", cudaGetErrorString(e));
+  }
   std::lock_guard<std::mutex> lk(mu);
   if (static_cast<int>(cache.size()) <= *dev) cache.resize(*dev + 1);
   DeviceInfo& d = cache[*dev];
@@ -76,6 +82,7 @@ spense_status current_device(int* dev, DeviceInfo* info) {
     if (cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, *dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess) {
       d.sms = 0;
+      cudaGetLastError();
       return fail(SPENSE_ERR_UNSUPPORTED, "cannot query device %d", *dev);
     }
   }
