@@ -31,10 +31,10 @@ template <bool kWide>
 __device__ __forceinline__ int expert_of(const void* ids, int i, int end, int E) {
   if (i >= end) return E;
   if constexpr (kWide) {
-    const long long v = __ldg(static_cast<const long long*>(ids) + i);
+    const long long v = ld_dep(static_cast<const long long*>(ids) + i);
     return v >= 0 && v < E ? static_cast<int>(v) : E;
   } else {
-    const int v = __ldg(static_cast<const int*>(ids) + i);
+    const int v = ld_dep(static_cast<const int*>(ids) + i);
     return v >= 0 && v < E ? v : E;
   }
 }
@@ -54,9 +54,9 @@ __device__ __forceinline__ uint32_t lanes_with(int e, int bits) {
 
 template <bool kWide, SortMode kMode>
 __global__ void __launch_bounds__(kSortThreads)
-    expert_sort_kernel(const void* __restrict__ ids, int n, int k, int E, int bits, int chunk,
+    expert_sort_kernel(const void* ids, int n, int k, int E, int bits, int chunk,
                        int32_t* __restrict__ offsets,
-                       int32_t* __restrict__ rows, int32_t* __restrict__ pos, int32_t* __restrict__ counts) {
+                       int32_t* __restrict__ rows, int32_t* __restrict__ pos, int32_t* counts) {
   extern __shared__ int hist[];  // [warps][E]: the warp's choices of an expert, then its first position
   __shared__ int warp_sum[kSortWarps];
   __shared__ int total_live;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kSortThreads)
       for (int u = 0; u < 4; ++u) {
         const int e = e0 + u * kSortWarps;
         v[u] = make_int4(0, 0, 0, 0);
-        if (e < E && c < chunks) v[u] = __ldcg(reinterpret_cast<const int4*>(counts + e * stride + c));
+        if (e < E && c < chunks) v[u] = ld_dep(reinterpret_cast<const int4*>(counts + e * stride + c));
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kSortThreads)
 // out[m][n] = bf16(sum over j of weights[m][j] * Y[pos[m][j]][n]) in fp32, j
 // ascending, choices with pos outside [0, T) left out (their weight is not
 // looked at). Bound by the gathered rows' bytes: 8191 x 8 rows of 5120 columns in 108
-// us, 0.97 of the measured copy rate.
+// us, 0.97 of the measured copy rate. The inputs are not __restrict__, so that they are
+// read by plain (coherent) loads: the grid before may still have been writing them.
 constexpr int kCombineThreads = 128;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -222,9 +223,9 @@ __device__ __forceinline__ int64_t token_of(int64_t i, unsigned int pieces, unsi
 
 // Rows 16-byte aligned: eight columns a thread.
 __global__ void __launch_bounds__(kCombineThreads)
-    expert_combine_kernel(const uint16_t* __restrict__ Y, int64_t T, int64_t N, int64_t ldy,
-                          const int32_t* __restrict__ pos, const float* __restrict__ weights, int64_t M, int k,
-                          uint16_t* __restrict__ out, int64_t ldo) {
+    expert_combine_kernel(const uint16_t* Y, int64_t T, int64_t N, int64_t ldy,
+                          const int32_t* pos, const float* weights, int64_t M, int k,
+                          uint16_t* out, int64_t ldo) {
   pdl_trigger();
   unsigned int piece;
   const int64_t m = token_of(static_cast<int64_t>(blockIdx.x) * kCombineThreads + threadIdx.x,
@@ -247,11 +248,11 @@ __global__ void __launch_bounds__(kCombineThreads)
       w[j] = 0.0f;
       v[j] = make_uint4(0u, 0u, 0u, 0u);
       if (j0 + j < k) {
-        const int64_t p = __ldg(pm + j0 + j);
+        const int64_t p = pm[j0 + j];
         live[j] = p >= 0 && p < T;
         if (live[j]) {
-          w[j] = __ldg(wm + j0 + j);
-          v[j] = __ldg(reinterpret_cast<const uint4*>(Y + p * ldy + n));
+          w[j] = wm[j0 + j];
+          v[j] = *reinterpret_cast<const uint4*>(Y + p * ldy + n);
         }
       }
     }
@@ -279,9 +280,9 @@ __global__ void __launch_bounds__(kCombineThreads)
 // rows 44 us; eight neighbouring columns a thread 53 us), 9456 rows of 5065 54 us.
 constexpr int kAnyPairs = 8, kAnyRows = 2;
 __global__ void __launch_bounds__(kCombineThreads, 8)
-    expert_combine_any_kernel(const uint16_t* __restrict__ Y, int64_t T, int64_t N, int64_t ldy,
-                              const int32_t* __restrict__ pos, const float* __restrict__ weights, int64_t M, int k,
-                              uint16_t* __restrict__ out, int64_t ldo) {
+    expert_combine_any_kernel(const uint16_t* Y, int64_t T, int64_t N, int64_t ldy,
+                              const int32_t* pos, const float* weights, int64_t M, int k,
+                              uint16_t* out, int64_t ldo) {
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   unsigned int window;
@@ -305,10 +306,10 @@ __global__ void __launch_bounds__(kCombineThreads, 8)
       live[j] = odd[j] = false;
       w[j] = 0.0f;
       if (j0 + j >= k) continue;
-      const int64_t p = __ldg(pm + j0 + j);
+      const int64_t p = pm[j0 + j];
       if (p < 0 || p >= T) continue;
       live[j] = true;
-      w[j] = __ldg(wm + j0 + j);
+      w[j] = wm[j0 + j];
       const uint16_t* row = Y + p * ldy + n0;
       odd[j] = (reinterpret_cast<uintptr_t>(row) & 2) != 0;
       const uint32_t* words = reinterpret_cast<const uint32_t*>(row - (odd[j] ? 1 : 0));
@@ -318,11 +319,11 @@ __global__ void __launch_bounds__(kCombineThreads, 8)
         x[j][i] = 0u;
         if (i == kAnyPairs && lane > 0) continue;  // behind a whole window's last pair, for lane 31
         if (c + 1 < cols || (odd[j] && c < cols))
-          x[j][i] = __ldg(words + 32 * i + lane);
+          x[j][i] = words[32 * i + lane];
         else if (c < cols)
-          x[j][i] = __ldg(row + c);
+          x[j][i] = row[c];
         else if (odd[j] && c == cols)
-          x[j][i] = __ldg(row + c - 1);  // the last column: the second value of the lane before
+          x[j][i] = row[c - 1];  // the last column: the second value of the lane before
       }
     }
 #pragma unroll

@@ -111,7 +111,7 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int E, int T
   lo = 0;
   hi = e < E ? T : 0;
   if (offsets == nullptr) return;
-  int most = e < E ? min(max(__ldg(offsets + e), 0), T) : 0;
+  int most = e < E ? min(max(ld_dep(offsets + e), 0), T) : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, most, o);
@@ -119,7 +119,7 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int E, int T
   }
   lo = max(most, carry);
   carry = __shfl_sync(0xffffffffu, lo, 31);
-  hi = e < E ? max(min(__ldg(offsets + e + 1), T), lo) : lo;
+  hi = e < E ? max(min(ld_dep(offsets + e + 1), T), lo) : lo;
 }
 
 // Inclusive sum over the warp.
@@ -811,7 +811,7 @@ constexpr int kTilePasses = 2;
 constexpr int kTileBlocks = 2 * kTilePasses;
 
 __global__ void __launch_bounds__(kTileThreads)
-    mx4_scale_tiles_kernel(const uint32_t* __restrict__ xs, const int32_t* __restrict__ offsets, int E, int T, int npad,
+    mx4_scale_tiles_kernel(const uint32_t* xs, const int32_t* offsets, int E, int T, int npad,
                            int groups, int kblocks, uint32_t* __restrict__ out) {
   ptx::griddep_launch_dependents();
   __shared__ int found[2];
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kTileThreads)
     const int g = 2 * kb0 + 4 * i + (threadIdx.x >> 6);
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-      v[i][w] = r0 + 32 * w < rows && g < groups ? __ldg(xs + static_cast<size_t>(g) * T + row0 + r0 + 32 * w) : 0u;
+      v[i][w] = r0 + 32 * w < rows && g < groups ? ld_dep(xs + static_cast<size_t>(g) * T + row0 + r0 + 32 * w) : 0u;
   }
   uint4* dst =
       reinterpret_cast<uint4*>(out) + static_cast<size_t>(rt) * kblocks * (kMx4XsTileBytes / 16) + half * 32 + lane;

@@ -81,7 +81,7 @@ struct RowTile {
 
 template <int kType, bool kWide>
 __global__ void __launch_bounds__(kThreads)
-    mx4_quantize_kernel(const void* __restrict__ X, int T, int K, int64_t ldx, const int32_t* __restrict__ rows,
+    mx4_quantize_kernel(const void* X, int T, int K, int64_t ldx, const int32_t* rows,
                         int M_src, uint8_t* __restrict__ Xq, uint8_t* __restrict__ xs, int words) {
   using Q = RowTile<kWide>;
   constexpr int kSize = kType == SPENSE_TYPE_F32 ? 4 : 2;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   int src = -1;  // the warp's source row, or none
   if (row < T) {
-    src = rows != nullptr ? __ldg(rows + row) : row;
+    src = rows != nullptr ? ld_dep(rows + row) : row;
     if (src >= M_src) src = -1;
   }
   const char* xrow = static_cast<const char*>(X) + static_cast<int64_t>(src) * ldx * kSize;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       raw[i][j] = make_uint4(0u, 0u, 0u, 0u);
-      if (src >= 0 && c < K) raw[i][j] = __ldg(reinterpret_cast<const uint4*>(xrow + c * kSize) + j);
+      if (src >= 0 && c < K) raw[i][j] = ld_dep(reinterpret_cast<const uint4*>(xrow + c * kSize) + j);
     }
   }
 #pragma unroll
@@ -226,7 +226,7 @@ __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&v)[8]) 
 // round to infinity.
 template <bool kF32, bool kWide>
 __global__ void __launch_bounds__(kThreads)
-    mx4_dequantize_kernel(const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ xs, int words, int T, int K,
+    mx4_dequantize_kernel(const uint8_t* Xq, const uint8_t* xs, int words, int T, int K,
                           void* __restrict__ Y) {
   using Q = RowTile<kWide>;
   pdl_trigger();
@@ -245,9 +245,9 @@ __global__ void __launch_bounds__(kThreads)
     codes[i] = make_uint2(0u, 0u);
     byte[i] = 0u;
     if (c < K) {
-      codes[i] = __ldg(reinterpret_cast<const uint2*>(Xq + (static_cast<int64_t>(row) * K + c) / 2));
-      byte[i] = words ? __ldg(xs + (static_cast<int64_t>(c / 128) * T + row) * 4 + (c / 32) % 4)
-                      : __ldg(xs + static_cast<int64_t>(row) * (K / 32) + c / 32);
+      codes[i] = ld_dep(reinterpret_cast<const uint2*>(Xq + (static_cast<int64_t>(row) * K + c) / 2));
+      byte[i] = words ? ld_dep(xs + (static_cast<int64_t>(c / 128) * T + row) * 4 + (c / 32) % 4)
+                      : ld_dep(xs + static_cast<int64_t>(row) * (K / 32) + c / 32);
     }
   }
 #pragma unroll
