@@ -19,10 +19,18 @@ import os
 import numpy as np
 import torch
 
-from torch._C import _cuda_getCurrentRawStream as _raw_stream
-from torch._C import _cuda_getDevice as _device_index
-
 from .build import LIB_PATH, TEST_LIB_PATH
+
+try:
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    from torch._C import _cuda_getDevice as _device_index
+except ImportError:  # a torch without CUDA, or without these private names
+
+    def _raw_stream(dev: int) -> int:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+    def _device_index() -> int:
+        return torch.cuda.current_device()
 
 SPENSE_OK = 0
 STATUS_NAMES = {
