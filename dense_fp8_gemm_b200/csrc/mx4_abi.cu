@@ -23,38 +23,38 @@ namespace {
 
 constexpr size_t kMx4Header = 256;  // workspace: status word, then pair mode's scale tiles
 
-// Shared memory of a CTA that has its SM to itself, or shares it with another.
-constexpr uint32_t kMx4Smem[2] = {232448u, 115200u};
+constexpr uint32_t kMx4Smem = 232448u;  // shared memory of a CTA, which has its SM to itself
 
-// Clusters of s CTAs, cps to a SM, that the device holds at once.
-int clusters_at_once(int s, int cps, int sms) {
+// Clusters of s CTAs that the device holds at once (148 SMs: 74, 45, 33, 26, 22, 15 and
+// 15 of 2 to 8).
+int clusters_at_once(int s, int sms) {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices][9][3];  // the number + 1; 0: not asked yet
+  static std::atomic<int> known[kDevices][9];  // the number + 1; 0: not asked yet
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return sms * cps / (s + 1);
-  if (dev < kDevices && known[dev][s][cps] > 0) return known[dev][s][cps] - 1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return sms / (s + 1);
+  if (dev < kDevices && known[dev][s] > 0) return known[dev][s] - 1;
   int n = 0;
-  if (mx4_max_clusters(s, kMx4Smem[cps - 1], &n) != cudaSuccess) {
+  if (mx4_max_clusters(s, kMx4Smem, &n) != cudaSuccess) {
     cudaGetLastError();
-    return sms * cps / (s + 1);
+    return sms / (s + 1);
   }
-  if (dev < kDevices) known[dev][s][cps] = n + 1;
+  if (dev < kDevices) known[dev][s] = n + 1;
   return n;
 }
 
 // Estimated time of a launch, in microseconds, from measured rates of this
 // kernel: a CTA takes 0.27 us a block and 0.0006 more a row of the tile (latency
 // of its ring), all CTAs together 12.4 TB/s from L2 and the weights 5.5 TB/s from
-// HBM; two CTAs on a SM take half as long again each; 3.2 us go before and after
-// the blocks, 6 ns a row into the epilogue, 0.8 us and 12 ns a row into the exchange
-// of a split tile's partials. Against a sweep of 5 shapes x 7 row counts (M 1 ..
-// 1024) x tiles x splits the choices by it are within 20 % of the best.
-double mx4_cost(int n, int split, int cps, int64_t tiles, int kblocks, double weight_bytes, int sms) {
+// HBM; 3.2 us go before and after the blocks, 6 ns a row into the epilogue, 0.8 us and
+// 12 ns a row into the exchange of a split tile's partials. Against a sweep of 5
+// shapes x 7 row counts (M 1 .. 1024) x tiles x splits the choices by it are within
+// 20 % of the best.
+double mx4_cost(int n, int split, int64_t tiles, int kblocks, double weight_bytes, int sms) {
   const int64_t ctas = tiles * split;
   const double waves = static_cast<double>((tiles + sms - 1) / sms);
   const double blocks = split == 1 ? waves * kblocks : (kblocks + split - 1) / split;
   const double l2 = (kMx4BlockBytes + n * 136.0) * static_cast<double>(std::min<int64_t>(ctas, sms)) / 12.4e6;
-  const double block = std::max(0.27 + 0.0006 * n, l2) * (cps == 2 ? 1.5 : 1.0);
+  const double block = std::max(0.27 + 0.0006 * n, l2);
   const double t = 3.2 + 0.006 * n + blocks * block + (split > 1 ? 0.8 + 0.012 * n : 0.0);
   return std::max(t, 3.2 + weight_bytes / 5.5e6) + 0.05 * t;
 }
@@ -117,11 +117,11 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
     return kMx4BlockBytes + static_cast<uint32_t>(pl.pair ? n / 2 : n) * 128u + (pl.pair ? kMx4XsTileBytes : 0u);
   };
   auto slot = [&](int n) { return pl.pair ? 0u : (n > 61 ? 2048u : 1024u); };
-  auto ring = [&](int n, int cps) {
+  auto ring = [&](int n) {
     const uint32_t fixed = 1024 + tail + kMx4XsSlots * slot(n);
-    return static_cast<int>(std::min<uint32_t>(12, (kMx4Smem[cps - 1] - fixed) / stage(n)));
+    return static_cast<int>(std::min<uint32_t>(12, (kMx4Smem - fixed) / stage(n)));
   };
-  pl.split = pl.ctas_per_sm = 1;
+  pl.split = 1;
   const double weight_bytes = static_cast<double>(active) * n_tiles * kblocks * kMx4BlockBytes;
   const int64_t m0 = ragged ? 1 : (T + kMx4MaxTile - 1) / kMx4MaxTile;
   double best = 0.0;
@@ -135,18 +135,16 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
     n = static_cast<int>(std::min<int64_t>(n, round_up(T, step)));
     const int64_t tiles = row_tiles(n) * n_tiles;
     for (int s = 1; s <= (pl.pair ? 1 : 8); ++s) {
-      const int cps = s > 1 && tiles * s > sms ? 2 : 1;
       if (s > 1) {
-        if (tiles * s > 2 * sms || kblocks < 2 * s || ring(n, cps) < 3 || n + 72 > 512 / cps) break;
+        if (tiles * s > sms || kblocks < 2 * s || ring(n) < 3) break;
         const size_t partials = static_cast<size_t>(s - 1) * round_up((n + s - 1) / s, 8) * 512;
-        if (partials > static_cast<size_t>(ring(n, cps)) * stage(n) || tiles > clusters_at_once(s, cps, sms)) continue;
+        if (partials > static_cast<size_t>(ring(n)) * stage(n) || tiles > clusters_at_once(s, sms)) continue;
       }
-      const double c = mx4_cost(n, s, cps, tiles, kblocks, weight_bytes, sms);
+      const double c = mx4_cost(n, s, tiles, kblocks, weight_bytes, sms);
       if (best == 0.0 || c < best) {
         best = c;
         pl.npad = n;
         pl.split = s;
-        pl.ctas_per_sm = cps;
       }
     }
     if (n <= step) break;
@@ -161,7 +159,7 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
       const double c = mx4_pair_cost(n, row_tiles(n) * ((n_tiles + 1) / 2), kblocks, weight_bytes, sms);
       if (c < best) {
         best = c;
-        pl.pair = pl.split = pl.ctas_per_sm = 1;
+        pl.pair = pl.split = 1;
         pl.npad = n;
       }
     }
@@ -174,12 +172,12 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
                                             : std::min<int64_t>(tiles, sms));
   pl.stage_bytes = stage(pl.npad);
   pl.xs_bytes = slot(pl.npad);
-  pl.stages = ring(pl.npad, pl.ctas_per_sm);
+  pl.stages = ring(pl.npad);
   // Tensor memory: two accumulators where a CTA has several tiles, and 16 or 24
   // scale columns a block in the ring.
-  const int sf_cols = pl.npad > 128 ? 24 : 16, cols = 512 / pl.ctas_per_sm;
-  pl.nacc = pl.split == 1 && 2 * pl.npad + 4 * sf_cols <= cols ? 2 : 1;
-  pl.stages = std::min(pl.stages, (cols - pl.nacc * pl.npad) / sf_cols);
+  const int sf_cols = pl.npad > 128 ? 24 : 16;
+  pl.nacc = pl.split == 1 && 2 * pl.npad + 4 * sf_cols <= 512 ? 2 : 1;
+  pl.stages = std::min(pl.stages, (512 - pl.nacc * pl.npad) / sf_cols);
   // Small tiles: two blocks a stage, which halves the waits and signals a block costs
   // the issuing warp (10240x5120 at one row 8.7 -> 7.5 us, 64-expert decode 37.9 ->
   // 36.2 us; with more than 64 rows the products cover them: the same either way).
@@ -194,8 +192,6 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
   pl.tmem_cols = 32;
   while (pl.tmem_cols < static_cast<uint32_t>(pl.nacc * pl.npad + pl.stages * pl.bps * sf_cols)) pl.tmem_cols <<= 1;
   pl.smem_bytes = 1024 + tail + kMx4XsSlots / pl.bps * pl.xs_bytes + static_cast<uint32_t>(pl.stages) * pl.stage_bytes;
-  // A CTA that takes more than half of the tensor memory has the SM to itself.
-  if (pl.tmem_cols > 256) pl.smem_bytes = std::max<uint32_t>(pl.smem_bytes, 122880u);
   pl.workspace_bytes = kMx4Header + (pl.pair ? static_cast<size_t>(pl.row_tiles) * kblocks * kMx4XsTileBytes : 0);
   *out = pl;
   return SPENSE_OK;

@@ -58,7 +58,7 @@ constexpr int kMx4MaxTile = 240;  // rows a tile takes: with three words in fron
 constexpr int kMx4PairRows = 256;  // the same of a pair, the most an MMA takes
 
 struct Mx4GemmPlan {
-  int npad, stages, nacc, bps, pair, split, ctas_per_sm, grid;
+  int npad, stages, nacc, bps, pair, split, grid;
   int64_t row_tiles;  // row tiles at most (all experts)
   size_t workspace_bytes;
   uint32_t stage_bytes, xs_bytes, tmem_cols, smem_bytes;
