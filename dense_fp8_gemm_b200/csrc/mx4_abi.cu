@@ -25,18 +25,19 @@ constexpr size_t kMx4Header = 256;  // workspace: status word, then pair mode's 
 
 constexpr uint32_t kMx4Smem = 232448u;  // shared memory of a CTA, which has its SM to itself
 
-// Clusters of s CTAs that the device holds at once (148 SMs: 74, 45, 33, 26, 22, 15 and
-// 15 of 2 to 8).
-int clusters_at_once(int s, int sms) {
+// Clusters of s CTAs that the current device holds at once (148 SMs: 74, 45, 33, 26, 22,
+// 15 and 15 of 2 to 8); without it (`ask` false) an estimate for so many SMs.
+int clusters_at_once(int s, int sms, bool ask) {
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices][9];  // the number + 1; 0: not asked yet
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return sms / (s + 1);
+  const int estimate = 10 * sms / (11 * s);
+  if (!ask || cudaGetDevice(&dev) != cudaSuccess) return estimate;
   if (dev < kDevices && known[dev][s] > 0) return known[dev][s] - 1;
   int n = 0;
   if (mx4_max_clusters(s, kMx4Smem, &n) != cudaSuccess) {
     cudaGetLastError();
-    return sms / (s + 1);
+    return estimate;
   }
   if (dev < kDevices) known[dev][s] = n + 1;
   return n;
@@ -103,7 +104,9 @@ int64_t mx4_pair_tiles(int64_t E, int64_t T, bool ragged) {
   return ragged ? E + T / kMx4PairLeast : (T + kMx4PairRows - 1) / kMx4PairRows + kMx4PairMore;
 }
 
-spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, Mx4GemmPlan* out) {
+// ask: `sms` are the current device's, which says how many clusters it holds.
+spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool ragged, int sms, bool ask,
+                              Mx4GemmPlan* out) {
   Mx4GemmPlan pl{};
   const uint32_t tail = static_cast<uint32_t>(round_up(kMx4BarrierBytes + 4 * (3 * static_cast<size_t>(E) + 1), 16));
   const int64_t active = ragged ? std::min(E, T) : 1;
@@ -138,7 +141,7 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
       if (s > 1) {
         if (tiles * s > sms || kblocks < 2 * s || ring(n) < 3) break;
         const size_t partials = static_cast<size_t>(s - 1) * round_up((n + s - 1) / s, 8) * 512;
-        if (partials > static_cast<size_t>(ring(n)) * stage(n) || tiles > clusters_at_once(s, sms)) continue;
+        if (partials > static_cast<size_t>(ring(n)) * stage(n) || tiles > clusters_at_once(s, sms, ask)) continue;
       }
       const double c = mx4_cost(n, s, tiles, kblocks, weight_bytes, sms);
       if (best == 0.0 || c < best) {
@@ -211,7 +214,7 @@ spense_status make_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bool
   for (const int64_t k : key) h = (h ^ static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull;
   Known& slot = known[h >> 58];
   if (slot.key != key) {
-    const spense_status st = search_mx4_plan(E, n_tiles, kblocks, T, ragged, sms, &slot.plan);
+    const spense_status st = search_mx4_plan(E, n_tiles, kblocks, T, ragged, sms, true, &slot.plan);
     if (st != SPENSE_OK) {
       slot.key = {};
       return st;
@@ -227,6 +230,20 @@ spense_status check_mx4_types(int64_t rows, int64_t K) {
     return fail(SPENSE_ERR_SHAPE, "%lld rows outside [0, 2^20]", (long long)rows);
   if (K < 32 || K > (1 << 20) || K % 32 != 0)
     return fail(SPENSE_ERR_SHAPE, "K = %lld must be a multiple of 32 in [32, 2^20]", (long long)K);
+  return SPENSE_OK;
+}
+
+// A packed weight's shape; its 128-row tiles and 256-column blocks.
+spense_status check_mx4_weight(int64_t E, int64_t N, int64_t K, int64_t* n_tiles, int64_t* kblocks) {
+  if (E < 1 || E > kMx4MaxExperts)
+    return fail(SPENSE_ERR_SHAPE, "%lld experts outside [1, %d]", (long long)E, kMx4MaxExperts);
+  if (N < 1 || N > (1 << 20)) return fail(SPENSE_ERR_SHAPE, "N = %lld outside [1, 2^20]", (long long)N);
+  const spense_status st = check_mx4_types(0, K);
+  if (st != SPENSE_OK) return st;
+  *n_tiles = (N + kMx4Rows - 1) / kMx4Rows;
+  *kblocks = (K + kMx4Cols - 1) / kMx4Cols;
+  if (E * *n_tiles * *kblocks > INT_MAX / (kMx4BlockBytes / 128))
+    return fail(SPENSE_ERR_SHAPE, "too many blocks for one weight (%lld)", (long long)(E * *n_tiles * *kblocks));
   return SPENSE_OK;
 }
 
@@ -401,14 +418,9 @@ spense_status spense_mx4_pack(const uint8_t* Wq, const uint8_t* w_scale, int64_t
   if (out == nullptr) return fail(SPENSE_ERR_ARG, "out is NULL");
   *out = nullptr;
   if (Wq == nullptr || w_scale == nullptr) return fail(SPENSE_ERR_ARG, "Wq or w_scale is NULL");
-  if (E < 1 || E > kMx4MaxExperts)
-    return fail(SPENSE_ERR_SHAPE, "%lld experts outside [1, %d]", (long long)E, kMx4MaxExperts);
-  if (N < 1 || N > (1 << 20)) return fail(SPENSE_ERR_SHAPE, "N = %lld outside [1, 2^20]", (long long)N);
-  spense_status st = check_mx4_types(0, K);
+  int64_t n_tiles = 0, kblocks = 0;
+  spense_status st = check_mx4_weight(E, N, K, &n_tiles, &kblocks);
   if (st != SPENSE_OK) return st;
-  const int64_t n_tiles = (N + kMx4Rows - 1) / kMx4Rows, kblocks = (K + kMx4Cols - 1) / kMx4Cols;
-  if (E * n_tiles * kblocks > INT_MAX / (kMx4BlockBytes / 128))
-    return fail(SPENSE_ERR_SHAPE, "too many blocks for one weight (%lld)", (long long)(E * n_tiles * kblocks));
   if (!aligned(Wq, 16)) return fail(SPENSE_ERR_ALIGN, "Wq is not 16-byte aligned");
   int dev = 0;
   DeviceInfo info;
@@ -473,6 +485,42 @@ size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M) {
   int64_t tiles = mx4_pair_tiles(Wp->E, M, true);
   if (Wp->E == 1) tiles = std::max(tiles, mx4_pair_tiles(1, M, false));
   return kMx4Header + static_cast<size_t>(tiles) * Wp->kblocks * kMx4XsTileBytes;
+}
+
+spense_status spense_mx4_plan_shapes(int64_t E, int64_t N, int64_t K, int64_t M, int grouped, int sms,
+                                     spense_mx4_plan_info* out) {
+  if (out == nullptr) return fail(SPENSE_ERR_ARG, "out is NULL");
+  if (sms < 1 || sms > 1024) return fail(SPENSE_ERR_ARG, "sms = %d outside [1, 1024]", sms);
+  if (E != 1 && !grouped) return fail(SPENSE_ERR_ARG, "%lld experts without grouped", (long long)E);
+  int64_t n_tiles = 0, kblocks = 0;
+  spense_status st = check_mx4_weight(E, N, K, &n_tiles, &kblocks);
+  if (st == SPENSE_OK) st = check_mx4_types(M, K);
+  if (st != SPENSE_OK) return st;
+  if (M == 0) return fail(SPENSE_ERR_SHAPE, "no rows, no launch");
+  int dev = 0, device_sms = 0;
+  const bool ask = cudaGetDevice(&dev) == cudaSuccess &&
+                   cudaDeviceGetAttribute(&device_sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+                   device_sms == sms;
+  if (!ask) cudaGetLastError();
+  Mx4GemmPlan pl;
+  st = search_mx4_plan(E, static_cast<int>(n_tiles), static_cast<int>(kblocks), M, grouped != 0, sms, ask, &pl);
+  if (st != SPENSE_OK) return st;
+  *out = spense_mx4_plan_info{};
+  out->npad = pl.npad;
+  out->pair = pl.pair;
+  out->split = pl.split;
+  out->grid = pl.grid;
+  out->stages = pl.stages;
+  out->blocks_per_stage = pl.bps;
+  out->nacc = pl.nacc;
+  out->tmem_cols = pl.tmem_cols;
+  out->smem_bytes = pl.smem_bytes;
+  out->stage_bytes = pl.stage_bytes;
+  out->n_tiles = n_tiles;
+  out->k_blocks = kblocks;
+  out->row_tiles = pl.row_tiles;
+  out->workspace_bytes = pl.workspace_bytes;
+  return ok();
 }
 
 spense_status spense_mx4_gemm(const spense_mx4_packed* Wp, const uint8_t* Xq, const uint8_t* x_scale, int64_t M,

@@ -50,8 +50,8 @@ SYMBOLS = (
     "spense_pack_rows", "spense_plan_shapes", "spense_gemm_grouped_host",
     "spense_gemm_grouped_host_workspace_size", "spense_glu_order", "spense_noalloc_status",
     "spense_mx4_quantize", "spense_mx4_dequantize", "spense_mx4_pack", "spense_mx4_free", "spense_mx4_get_info",
-    "spense_mx4_workspace_size", "spense_mx4_gemm", "spense_mx4_gemm_experts", "spense_expert_sort",
-    "spense_expert_sort_workspace_size", "spense_expert_combine",
+    "spense_mx4_workspace_size", "spense_mx4_plan_shapes", "spense_mx4_gemm", "spense_mx4_gemm_experts",
+    "spense_expert_sort", "spense_expert_sort_workspace_size", "spense_expert_combine",
 )
 GEMM_X_PACKED_ORDER = 1
 GEMM_HOST_X = 2
@@ -83,6 +83,14 @@ class PackedInfo(ctypes.Structure):
 class Mx4Info(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("n_tiles", ctypes.c_int64),
                 ("k_blocks", ctypes.c_int64), ("blocks", ctypes.c_void_p), ("weight_bytes", ctypes.c_uint64)]
+
+
+class Mx4PlanInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("npad", "pair", "split", "grid", "stages", "blocks_per_stage",
+                                              "nacc")] + \
+               [(n, ctypes.c_uint32) for n in ("tmem_cols", "smem_bytes", "stage_bytes")] + \
+               [(n, ctypes.c_int64) for n in ("n_tiles", "k_blocks", "row_tiles")] + \
+               [("workspace_bytes", ctypes.c_uint64)]
 
 
 _lib = None
@@ -152,6 +160,7 @@ def lib() -> ctypes.CDLL:
     L.spense_mx4_get_info.argtypes = [P, ctypes.POINTER(Mx4Info)]
     L.spense_mx4_workspace_size.argtypes = [P, I64]
     L.spense_mx4_workspace_size.restype = SZ
+    L.spense_mx4_plan_shapes.argtypes = [I64, I64, I64, I64, I, I, ctypes.POINTER(Mx4PlanInfo)]
     L.spense_mx4_gemm.argtypes = [P, P, P, I64, P, I64, P, SZ, P]
     L.spense_mx4_gemm_experts.argtypes = [P, P, P, I64, P, P, I64, P, SZ, P]
     L.spense_expert_sort.argtypes = [P, I, I64, I64, I64, P, P, P, P, SZ, P]
@@ -763,6 +772,14 @@ def mx4_workspace_size(pw: Mx4Weight, M: int) -> int:
     if n == 0:
         _check(1, "spense_mx4_workspace_size")
     return int(n)
+
+
+def mx4_plan_shapes(E: int, N: int, K: int, M: int, grouped: bool = False, sms: int = 148) -> dict:
+    """spense_mx4_plan_shapes: the launch plan of a product of M rows with a weight of
+    E matrices [N, K] (grouped: by expert), from shapes alone, as a dict of its fields."""
+    info = Mx4PlanInfo()
+    _check(lib().spense_mx4_plan_shapes(E, N, K, M, int(grouped), sms, ctypes.byref(info)), "spense_mx4_plan_shapes")
+    return {name: getattr(info, name) for name, _ in Mx4PlanInfo._fields_}
 
 
 class PreparedMx4Gemm:

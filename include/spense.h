@@ -531,6 +531,32 @@ SPENSE_API spense_status spense_mx4_get_info(const spense_mx4_packed* Wp, spense
 /* Bytes of workspace the MXFP4 products need for M rows or fewer; 0 on a bad argument. */
 SPENSE_API size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M);
 
+/* The launch plan a product of M rows would get, from shapes alone (no device memory, no
+ * GPU needed; for inspection and tests, as spense_plan_shapes is for the FP8
+ * products): a weight of E matrices [N][K], `grouped` 0 for spense_mx4_gemm (E = 1) and 1
+ * for spense_mx4_gemm_experts, on a device with `sms` SMs. Where the current device has as
+ * many, it says how many clusters it holds at once, and the plan is the one it would
+ * run; else that number is estimated. Shape rules as for spense_mx4_pack and the
+ * products, M at least 1. Errors: ARG, SHAPE. */
+typedef struct spense_mx4_plan_info {
+  int32_t npad;              /* activation rows of a tile (the MMA N, or a pair's) */
+  int32_t pair;              /* 1: CTA pairs share MMAs of 256 weight rows */
+  int32_t split;             /* CTAs of a cluster that split one tile's K range (1: none) */
+  int32_t grid;              /* CTAs */
+  int32_t stages;            /* shared-memory ring stages per CTA */
+  int32_t blocks_per_stage;  /* 256-column blocks a stage holds, 1 or 2 */
+  int32_t nacc;              /* accumulator buffers in tensor memory */
+  uint32_t tmem_cols;        /* tensor-memory columns allocated per CTA */
+  uint32_t smem_bytes;       /* dynamic shared memory per CTA */
+  uint32_t stage_bytes;      /* bytes of one ring stage */
+  int64_t n_tiles, k_blocks; /* 128-row tiles, 256-column blocks of one matrix */
+  int64_t row_tiles;         /* tiles of activation rows, with experts the most there can be */
+  uint64_t workspace_bytes;  /* what this launch needs (spense_mx4_workspace_size: M rows or fewer) */
+} spense_mx4_plan_info;
+
+SPENSE_API spense_status spense_mx4_plan_shapes(int64_t E, int64_t N, int64_t K, int64_t M, int grouped, int sms,
+                                                spense_mx4_plan_info* out);
+
 /*
  * spense_mx4_gemm — Y[m][n] = bf16(sum_k X[m][k] W[n][k]) of MXFP4 activations and
  * a packed MXFP4 weight with E = 1; products and sums in fp32 (a fixed order:
