@@ -233,6 +233,15 @@ spense_status check_mx4_types(int64_t rows, int64_t K) {
   return SPENSE_OK;
 }
 
+// The activation scales' words of a product's rows are counted in 32 bits.
+spense_status check_mx4_words(int64_t rows, int64_t K) {
+  const int64_t words = (K + 127) / 128 * rows;
+  if (words > INT_MAX)
+    return fail(SPENSE_ERR_SHAPE, "%lld words of activation scales (%lld rows of K = %lld), at most 2^31 - 1",
+                (long long)words, (long long)rows, (long long)K);
+  return SPENSE_OK;
+}
+
 // A packed weight's shape; its 128-row tiles and 256-column blocks.
 spense_status check_mx4_weight(int64_t E, int64_t N, int64_t K, int64_t* n_tiles, int64_t* kblocks) {
   if (E < 1 || E > kMx4MaxExperts)
@@ -252,6 +261,8 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
                       void* stream) {
   if (h == nullptr) return fail(SPENSE_ERR_ARG, "Wp is NULL");
   if (T < 0 || T > kMx4MaxRows) return fail(SPENSE_ERR_SHAPE, "%lld rows outside [0, 2^20]", (long long)T);
+  spense_status st = check_mx4_words(T, h->K);
+  if (st != SPENSE_OK) return st;
   if (T > 0 && (Xq == nullptr || x_scale == nullptr || Y == nullptr))
     return fail(SPENSE_ERR_ARG, "Xq, x_scale or Y is NULL");
   if (ldy < h->N || ldy > (1 << 30))
@@ -262,7 +273,7 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
   if (!aligned(workspace, 256)) return fail(SPENSE_ERR_ALIGN, "workspace is not 256-byte aligned");
   int dev = 0;
   DeviceInfo info;
-  spense_status st = current_device(&dev, &info);
+  st = current_device(&dev, &info);
   if (st != SPENSE_OK) return st;
   if (dev != h->device)
     return fail(SPENSE_ERR_ARG, "handle was packed on device %d, current device is %d", h->device, dev);
@@ -288,8 +299,6 @@ spense_status run_mx4(const spense_mx4_packed* h, const uint8_t* Xq, const uint8
     if (r != CUDA_SUCCESS) return fail(SPENSE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
   const int64_t groups = (h->K + 127) / 128;
-  if (groups * T > INT_MAX)
-    return fail(SPENSE_ERR_SHAPE, "too many activation scales for one launch (%lld words)", (long long)(groups * T));
   for (int i = 0; i < 2; ++i) {
     const cuuint64_t dims[1] = {static_cast<cuuint64_t>(groups * T)};
     const cuuint64_t strides[1] = {0};  // a one-dimensional map has none
@@ -480,6 +489,7 @@ size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M) {
     fail(SPENSE_ERR_ARG, "Wp is NULL or M outside [0, 2^20]");
     return 0;
   }
+  if (check_mx4_words(M, Wp->K) != SPENSE_OK) return 0;
   // A weight of one expert serves both products, which may be planned differently.
   // Enough for fewer rows too, whose tiles may be more.
   int64_t tiles = mx4_pair_tiles(Wp->E, M, true);
@@ -495,6 +505,7 @@ spense_status spense_mx4_plan_shapes(int64_t E, int64_t N, int64_t K, int64_t M,
   int64_t n_tiles = 0, kblocks = 0;
   spense_status st = check_mx4_weight(E, N, K, &n_tiles, &kblocks);
   if (st == SPENSE_OK) st = check_mx4_types(M, K);
+  if (st == SPENSE_OK) st = check_mx4_words(M, K);
   if (st != SPENSE_OK) return st;
   if (M == 0) return fail(SPENSE_ERR_SHAPE, "no rows, no launch");
   int dev = 0, device_sms = 0;

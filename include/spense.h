@@ -528,7 +528,8 @@ typedef struct spense_mx4_info {
 
 SPENSE_API spense_status spense_mx4_get_info(const spense_mx4_packed* Wp, spense_mx4_info* info);
 
-/* Bytes of workspace the MXFP4 products need for M rows or fewer; 0 on a bad argument. */
+/* Bytes of workspace the MXFP4 products need for M rows or fewer; 0 on a bad argument,
+ * an M that the products refuse among them. */
 SPENSE_API size_t spense_mx4_workspace_size(const spense_mx4_packed* Wp, int64_t M);
 
 /* The launch plan a product of M rows would get, from shapes alone (no device memory, no
@@ -564,7 +565,7 @@ SPENSE_API spense_status spense_mx4_plan_shapes(int64_t E, int64_t N, int64_t K,
  *   Xq, x_scale  device, codes [M][K / 2] and scale bytes in the words layout,
  *                16-byte aligned, as spense_mx4_quantize writes them. A scale
  *                byte 255 makes its row of Y NaN.
- *   M            0 .. 2^20 rows (0: nothing to do).
+ *   M            0 .. 2^20 rows (0: nothing to do), M ceil(K / 128) < 2^31.
  *   Y            device, bf16, row m at Y + m * ldy, N <= ldy <= 2^30, 16-byte
  *                aligned (16-byte stores are used when ldy % 8 == 0).
  *   workspace    at least spense_mx4_workspace_size bytes, 256-byte aligned,
@@ -582,7 +583,7 @@ SPENSE_API spense_status spense_mx4_gemm(const spense_mx4_packed* Wp, const uint
 /*
  * spense_mx4_gemm_experts — the same product grouped by expert: for every expert
  * e, rows offsets[e] .. offsets[e + 1] of X with weight e.
- *   T        rows of X, x_scale (its layout's R) and Y.
+ *   T        rows of X, x_scale (its layout's R) and Y (limits as M above).
  *   offsets  device int32 [E + 1], ascending, within [0, T] (read on the device
  *            only, so nothing is synchronized; values outside [0, T] are cut to it,
  *            and one below an earlier one counts as that). An expert may have no

@@ -70,3 +70,16 @@ def test_the_kernel_runs_the_reported_plan(M, N, K, kind):
     got = y[torch.from_numpy(ms).cuda()][:, torch.from_numpy(ns).cuda()].double().cpu().numpy()
     assert (np.abs(got - want) <= tol).all()
     pw.free()
+
+
+def test_workspace_size_refuses_what_the_products_refuse():
+    """More words of activation scales than 32 bits count."""
+    K = 1 << 20
+    pw = spense.mx4_pack(torch.zeros((1, K // 2), dtype=torch.uint8, device="cuda"),
+                         torch.full((1, K // 32), 127, dtype=torch.uint8, device="cuda"))
+    assert spense.mx4_workspace_size(pw, 262143) > 256
+    for M in (262144, 1 << 20):
+        with pytest.raises(spense.SpenseError, match="words of activation scales"):
+            spense.mx4_workspace_size(pw, M)
+        assert spense.lib().spense_mx4_gemm(pw.handle, 0x1000, 0x1000, M, 0x1000, 1, 0x1000, 1 << 40, None) == 2
+    pw.free()

@@ -100,6 +100,12 @@ def test_refusals():
         with pytest.raises(spense.SpenseError) as e:
             spense.mx4_plan_shapes(**{**dict(E=2, N=128, K=256, M=4, grouped=True), **bad})
         assert e.value.code == 2, bad
+    # a product's words of activation scales: at most 2^31 - 1
+    assert spense.mx4_plan_shapes(1, 1, 1 << 20, 262143)["npad"] > 0
+    for M, K in ((262144, 1 << 20), (1 << 20, 2048 * 128)):
+        with pytest.raises(spense.SpenseError, match="words of activation scales") as e:
+            spense.mx4_plan_shapes(1, 1, K, M)
+        assert e.value.code == 2
     for bad in (dict(sms=0), dict(sms=1025), dict(E=2, grouped=False)):
         with pytest.raises(spense.SpenseError) as e:
             spense.mx4_plan_shapes(**{**dict(E=1, N=128, K=256, M=4, grouped=True), **bad})
