@@ -221,9 +221,9 @@ __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&v)[8]) 
 // row; kWide: eight rows a CTA, two pieces a warp, all loads first; else eight
 // pieces of one row. 32768 rows of 5120 take 71 us, 6.0 TB/s (16-byte stores 86 us).
 //
-// Every value is exact in the output type (three significant bits; 2^-128 at
-// least) up to 6 x 2^125; larger ones, which the quantiser never makes, may
-// round to infinity.
+// Every value is exact in the output type (two significant bits; 2^-128 at least)
+// below 2^128; larger ones (4 and 6 times 2^126, 2 and more times 2^127), which the
+// quantiser never makes, become infinite.
 template <bool kF32, bool kWide>
 __global__ void __launch_bounds__(kThreads)
     mx4_dequantize_kernel(const uint8_t* Xq, const uint8_t* xs, int words, int T, int K,

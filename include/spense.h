@@ -492,8 +492,9 @@ SPENSE_API spense_status spense_mx4_quantize(const void* X, int x_type, int64_t 
 
 /*
  * spense_mx4_dequantize — the values of M rows of codes and scales, as bf16 or
- * fp32 (y_type), contiguous [M][K]. Exact for every scale byte below 253 (6 2^126
- * and more may round to infinity); scale byte 255 gives NaN.
+ * fp32 (y_type), contiguous [M][K]. Exact, except that magnitudes of 2^128 and more
+ * (codes of 4 and 6 with scale byte 253, of 2 and more with 254) become infinite;
+ * scale byte 255 gives NaN.
  * Asynchronous on `stream`. Errors: ARG, SHAPE, ALIGN, UNSUPPORTED, CUDA.
  */
 SPENSE_API spense_status spense_mx4_dequantize(const uint8_t* Xq, const uint8_t* x_scale, int64_t M, int64_t K,
