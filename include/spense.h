@@ -562,7 +562,10 @@ SPENSE_API spense_status spense_mx4_plan_shapes(int64_t E, int64_t N, int64_t K,
 /*
  * spense_mx4_gemm — Y[m][n] = bf16(sum_k X[m][k] W[n][k]) of MXFP4 activations and
  * a packed MXFP4 weight with E = 1; products and sums in fp32 (a fixed order:
- * repeatable bit for bit).
+ * repeatable bit for bit). Both scales count in full: a product is infinite only where
+ * the two values' product is 2^128 or more, and vanishes only below fp32's and bf16's
+ * subnormals. Where products of that size meet others of the opposite sign, Y may be
+ * infinite, NaN or their finite sum.
  *   Xq, x_scale  device, codes [M][K / 2] and scale bytes in the words layout,
  *                16-byte aligned, as spense_mx4_quantize writes them. A scale
  *                byte 255 makes its row of Y NaN.
