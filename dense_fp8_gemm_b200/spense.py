@@ -848,7 +848,10 @@ def mx4_gemm_experts(pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, off
 
 @functools.lru_cache(maxsize=256)
 def _sort_workspace(M: int, k: int, E: int) -> int:
-    return int(lib().spense_expert_sort_workspace_size(M, k, E))
+    n = int(lib().spense_expert_sort_workspace_size(M, k, E))
+    if n == 0:  # raised, so that it is not kept: the next refusal asks again for the reason
+        _check(2, "spense_expert_sort")
+    return n
 
 
 def expert_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None,
@@ -866,8 +869,6 @@ def expert_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, 
     n = M * k
     if offsets is None or rows is None or pos is None or workspace is None:
         need = _sort_workspace(M, k, E) // 4
-        if need == 0:
-            _check(2, "spense_expert_sort")
         with _made_on(stream):
             made = torch.empty(need + 2 * n + E + 1, dtype=torch.int32, device=ids.device)
         ws, r, p, o = made.split_with_sizes((need, n, n, E + 1))
