@@ -741,6 +741,7 @@ class Mx4Weight:
     def free(self):
         if self._h is not None and self._h.value:
             _check(lib().spense_mx4_free(self._h), "spense_mx4_free")
+            self._h.value = None  # prepared products hold this object: the library then refuses them
         self._h = None
 
     def __del__(self):
