@@ -11,7 +11,6 @@ until the work there is done.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -324,23 +323,17 @@ def new_workspace(nbytes: int, device=None) -> torch.Tensor:
     return torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
 
 
-def _made_on(stream):
-    """Where a call makes the buffers that it was not given: on the stream it launches
-    on. Made on another one, their memory (and a workspace's zero fill) would be
-    ordered by that one's work, before the call and once they are dropped."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
 def gemm(pw: PackedWeight, X: torch.Tensor, x_scale: torch.Tensor, Y: torch.Tensor | None = None,
          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """spense_gemm: Y [M, N] bf16 = X [M, K] e4m3 x packed W^T, scaled."""
+    if stream is not None and (Y is None or workspace is None):
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return gemm(pw, X, x_scale, Y, workspace)
     M = X.shape[0]
-    if Y is None or workspace is None:
-        with _made_on(stream):
-            if Y is None:
-                Y = torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device)
-            if workspace is None:
-                workspace = new_workspace(workspace_size(pw, M), X.device)
+    if Y is None:
+        Y = torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device)
+    if workspace is None:
+        workspace = new_workspace(workspace_size(pw, M), X.device)
     code = lib().spense_gemm(pw.handle, _dev_ptr(X, torch.uint8, "X"),
                              _dev_ptr(x_scale, torch.float32, "x_scale"), M,
                              _dev_ptr(Y, torch.bfloat16, "Y"), _dev_ptr(workspace, torch.uint8, "workspace"),
@@ -387,13 +380,14 @@ def gemm_grouped(pws, X: torch.Tensor, x_scale: torch.Tensor, Ys=None, workspace
     (from quantize(..., order=pw)). ldy: per-output row strides in elements,
     with Ys given as flat device tensors (views into a wider output). Returns
     the list of outputs."""
+    if stream is not None and (Ys is None or workspace is None):
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return gemm_grouped(pws, X, x_scale, Ys, workspace, None, flags, ldy)
     M = X.shape[0]
-    if Ys is None or workspace is None:
-        with _made_on(stream):
-            if Ys is None:
-                Ys = [torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device) for pw in pws]
-            if workspace is None:
-                workspace = new_workspace(grouped_workspace_size(pws, M), X.device)
+    if Ys is None:
+        Ys = [torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device) for pw in pws]
+    if workspace is None:
+        workspace = new_workspace(grouped_workspace_size(pws, M), X.device)
     yarr = (ctypes.c_void_p * len(pws))()
     strided = any(not Y.is_contiguous() for Y in Ys)
     if strided and ldy is None:
@@ -503,13 +497,14 @@ def quantize(X: torch.Tensor, order: PackedWeight | None = None, Xq: torch.Tenso
     (s = absmax / 448 in fp32, e4m3 round-to-nearest-even, saturating), with the
     columns in `order`'s packed order when a packed weight is given. Returns
     (Xq uint8 [M, K], x_scale float32 [M])."""
+    if stream is not None and (Xq is None or x_scale is None):
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return quantize(X, order, Xq, x_scale)
     M, K = X.shape
-    if Xq is None or x_scale is None:
-        with _made_on(stream):
-            if Xq is None:
-                Xq = torch.empty((M, K), dtype=torch.uint8, device=X.device)
-            if x_scale is None:
-                x_scale = torch.empty((M,), dtype=torch.float32, device=X.device)
+    if Xq is None:
+        Xq = torch.empty((M, K), dtype=torch.uint8, device=X.device)
+    if x_scale is None:
+        x_scale = torch.empty((M,), dtype=torch.float32, device=X.device)
     code = lib().spense_quantize(_dev_ptr(X, torch.bfloat16, "X"), M, K, None if order is None else order.handle,
                                  _dev_ptr(Xq, torch.uint8, "Xq"), _dev_ptr(x_scale, torch.float32, "x_scale"),
                                  _stream(stream))
@@ -574,13 +569,14 @@ def score_glu(down: torch.Tensor, s_down: torch.Tensor, h_in: torch.Tensor, h_mi
     GLU MLP. gate/up: uint8 e4m3 [I, H] (+ fp32 row scales [I]); down: uint8 e4m3
     [H, I] (+ fp32 [H]); h_in [H], h_mid [I] fp32 Hessian diagonals. Returns
     score fp32 [I]."""
+    if stream is not None and (score is None or workspace is None):
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return score_glu(down, s_down, h_in, h_mid, gate, s_gate, up, s_up, score, workspace)
     H, I = down.shape
-    if score is None or workspace is None:
-        with _made_on(stream):
-            if score is None:
-                score = torch.empty((I,), dtype=torch.float32, device=down.device)
-            if workspace is None:
-                workspace = new_workspace(max(256, int(lib().spense_score_workspace_size(I, H))), down.device)
+    if score is None:
+        score = torch.empty((I,), dtype=torch.float32, device=down.device)
+    if workspace is None:
+        workspace = new_workspace(max(256, int(lib().spense_score_workspace_size(I, H))), down.device)
     code = lib().spense_score_glu(_dev_ptr(gate, torch.uint8, "gate"), _dev_ptr(s_gate, torch.float32, "s_gate"),
                                   _dev_ptr(up, torch.uint8, "up"), _dev_ptr(s_up, torch.float32, "s_up"), I, H,
                                   _dev_ptr(down, torch.uint8, "down"), _dev_ptr(s_down, torch.float32, "s_down"),
@@ -594,10 +590,12 @@ def score_glu(down: torch.Tensor, s_down: torch.Tensor, h_in: torch.Tensor, h_mi
 def select_dense(score: torch.Tensor, Kd: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """spense_select_dense: the Kd largest scores (ties to the lower index) as
     ascending int32 indices on the device."""
+    if stream is not None and out is None:
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return select_dense(score, Kd)
     I = score.shape[0]
     if out is None:
-        with _made_on(stream):
-            out = torch.empty((Kd,), dtype=torch.int32, device=score.device)
+        out = torch.empty((Kd,), dtype=torch.int32, device=score.device)
     code = lib().spense_select_dense(_dev_ptr(score, torch.float32, "score"), I, int(Kd),
                                      _dev_ptr(out, torch.int32, "dense_idx") if Kd > 0 else None, _stream(stream))
     _check(code, "spense_select_dense")
@@ -655,6 +653,9 @@ def mx4_quantize(X: torch.Tensor, rows: torch.Tensor | None = None, scale_rows: 
     outside [0, M) leave their output row as it was). Returns (Xq uint8
     [T, K / 2], x_scale uint8): scales as words [ceil(K / 128), T, 4], or
     [T, K / 32] with scale_rows (the layout mx4_pack takes)."""
+    if stream is not None and (Xq is None or x_scale is None):
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return mx4_quantize(X, rows, scale_rows, Xq, x_scale)
     dtype = X.dtype
     if dtype not in MX4_TYPES:
         raise TypeError(f"X must be bfloat16, float16 or float32, got {dtype}")
@@ -665,14 +666,12 @@ def mx4_quantize(X: torch.Tensor, rows: torch.Tensor | None = None, scale_rows: 
     x, ldx = _rows_addr(X, dtype, dev, "X", M, K)
     T, r = (M, None) if rows is None else (rows.shape[0], _addr(rows, torch.int32, dev, "rows"))
     if Xq is None:
-        with _made_on(stream):
-            Xq = torch.empty(T, K // 2, dtype=torch.uint8, device=X.device)
+        Xq = torch.empty(T, K // 2, dtype=torch.uint8, device=X.device)
     elif Xq.shape != (T, K // 2):
         raise ValueError(f"Xq must be [{T}, {K // 2}], got {tuple(Xq.shape)}")
     if x_scale is None:
-        with _made_on(stream):
-            x_scale = torch.empty(*((T, K // 32) if scale_rows else (-(-K // 128), T, 4)), dtype=torch.uint8,
-                                  device=X.device)
+        x_scale = torch.empty(*((T, K // 32) if scale_rows else (-(-K // 128), T, 4)), dtype=torch.uint8,
+                              device=X.device)
     elif scale_rows and x_scale.shape != (T, K // 32):
         raise ValueError(f"x_scale must be [{T}, {K // 32}], got {tuple(x_scale.shape)}")
     flags = MX4_SCALE_ROWS if scale_rows else _scale_flags(x_scale, T, K)
@@ -687,14 +686,16 @@ def mx4_dequantize(Xq: torch.Tensor, x_scale: torch.Tensor, dtype=torch.bfloat16
                    stream=None) -> torch.Tensor:
     """spense_mx4_dequantize: the values [M, K] of codes [M, K / 2] and their scales
     (either layout), as bfloat16 or float32."""
+    if stream is not None and out is None:
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return mx4_dequantize(Xq, x_scale, dtype)
     if Xq.dim() != 2:
         raise ValueError("Xq must be 2-D")
     dev = _device_index()
     M, K = Xq.shape
     K *= 2
     if out is None:
-        with _made_on(stream):
-            out = torch.empty(M, K, dtype=dtype, device=Xq.device)
+        out = torch.empty(M, K, dtype=dtype, device=Xq.device)
     if out.shape != (M, K) or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"the output must be bfloat16 or float32 [{M}, {K}], got {out.dtype} {tuple(out.shape)}")
     code = lib().spense_mx4_dequantize(_addr(Xq, torch.uint8, dev, "Xq"), _addr(x_scale, torch.uint8, dev, "x_scale"),
@@ -822,12 +823,13 @@ def mx4_gemm(pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, Y: torch.Te
              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """spense_mx4_gemm: Y [M, N] bf16 = X x W^T of MXFP4 activations (mx4_quantize) and
     a packed weight. Y may be a column slice of a wider tensor."""
-    if Y is None or workspace is None:
-        with _made_on(stream):
-            if Y is None:
-                Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
-            if workspace is None:
-                workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
+    if stream is not None and (Y is None or workspace is None):
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return mx4_gemm(pw, Xq, x_scale, Y, workspace)
+    if Y is None:
+        Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
+    if workspace is None:
+        workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
     PreparedMx4Gemm(pw, Xq, x_scale, Y, workspace)(stream)
     return Y
 
@@ -837,12 +839,13 @@ def mx4_gemm_experts(pw: Mx4Weight, Xq: torch.Tensor, x_scale: torch.Tensor, off
     """spense_mx4_gemm_experts: rows offsets[e] .. offsets[e + 1] (device int32
     [E + 1]) of X with expert e's weight. Rows outside every range are left as
     they were in Y (unset in a Y made here)."""
-    if Y is None or workspace is None:
-        with _made_on(stream):
-            if Y is None:
-                Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
-            if workspace is None:
-                workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
+    if stream is not None and (Y is None or workspace is None):
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return mx4_gemm_experts(pw, Xq, x_scale, offsets, Y, workspace)
+    if Y is None:
+        Y = torch.empty((Xq.shape[0], pw.N), dtype=torch.bfloat16, device=Xq.device)
+    if workspace is None:
+        workspace = new_workspace(mx4_workspace_size(pw, Xq.shape[0]), Xq.device)
     PreparedMx4Gemm(pw, Xq, x_scale, Y, workspace, offsets)(stream)
     return Y
 
@@ -862,6 +865,9 @@ def expert_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, 
     [M k]: the token of every slot, -1 behind the last; pos int32 [M, k]: the slot
     of every choice, -1 for one left out). What is not given is made here, in one
     allocation."""
+    if stream is not None and (offsets is None or rows is None or pos is None or workspace is None):
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return expert_sort(ids, E, offsets, rows, pos, workspace)
     dtype = ids.dtype
     if ids.dim() != 2 or dtype not in (torch.int32, torch.int64):
         raise ValueError(f"ids must be int32 or int64 [M, k], got {dtype} {tuple(ids.shape)}")
@@ -870,8 +876,7 @@ def expert_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, 
     n = M * k
     if offsets is None or rows is None or pos is None or workspace is None:
         need = _sort_workspace(M, k, E) // 4
-        with _made_on(stream):
-            made = torch.empty(need + 2 * n + E + 1, dtype=torch.int32, device=ids.device)
+        made = torch.empty(need + 2 * n + E + 1, dtype=torch.int32, device=ids.device)
         ws, r, p, o = made.split_with_sizes((need, n, n, E + 1))
         workspace = ws if workspace is None else workspace
         rows = r if rows is None else rows
@@ -894,6 +899,9 @@ def expert_combine(Y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, ou
     """spense_expert_combine: out[m] = sum_j weights[m, j] Y[pos[m, j]] in fp32, rounded
     to bf16; choices with pos outside Y's rows are left out. Y and out may be
     column slices of wider tensors."""
+    if stream is not None and out is None:
+        with torch.cuda.stream(stream):  # what the call makes belongs to its stream
+            return expert_combine(Y, pos, weights)
     if Y.dim() != 2 or pos.dim() != 2 or weights.shape != pos.shape:
         raise ValueError(f"Y [T, N], pos and weights [M, k] expected, got {tuple(Y.shape)}, {tuple(pos.shape)} and "
                          f"{tuple(weights.shape)}")
@@ -902,8 +910,7 @@ def expert_combine(Y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, ou
     M, k = pos.shape
     y, ldy = _rows_addr(Y, torch.bfloat16, dev, "Y", T, N)
     if out is None:
-        with _made_on(stream):
-            out = torch.empty(M, N, dtype=torch.bfloat16, device=Y.device)
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=Y.device)
     elif out.shape != (M, N):
         raise ValueError(f"out must be [{M}, {N}], got {tuple(out.shape)}")
     o, ldo = _rows_addr(out, torch.bfloat16, dev, "out", M, N)
