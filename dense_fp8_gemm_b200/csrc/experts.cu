@@ -15,8 +15,9 @@ namespace {
 // A counting sort: position of choice i = (choices of smaller experts) +
 // (earlier choices of the same expert). The choices are cut into chunks of one
 // CTA each, and a chunk into 32 contiguous runs of one warp each; a warp takes
-// its run 32 choices at a time and finds the equal ones among them by ballots, so nothing depends on the order in which warps or CTAs
-// arrive and the result is the stable one.
+// its run 32 choices at a time and finds the equal ones among them by ballots, so
+// nothing depends on the order in which warps or CTAs arrive and the result is the
+// stable one.
 //   kSingle  the one chunk: counts, offsets and positions in one launch.
 //   kCount   counts of a chunk into counts[E][chunks].
 //   kPlace   recounts the chunk and takes its bases from all chunks' counts, a
@@ -204,8 +205,9 @@ __global__ void __launch_bounds__(kSortThreads)
 // ---------------------------------------------------------------- combine
 // out[m][n] = bf16(sum over j of weights[m][j] * Y[pos[m][j]][n]) in fp32, j
 // ascending, choices with pos outside [0, T) left out (their weight is not
-// looked at). Bound by the gathered rows' bytes: 8191 x 8 rows of 5120 columns in 108
-// us, 0.97 of the measured copy rate. The inputs are not __restrict__, so that they are
+// looked at). Bound by the gathered rows' bytes: 8191 x 8 rows of 5120 columns in 116
+// us, 6.5 TB/s or 0.99 of the measured copy rate, and 108 us (0.97) with a tenth of the
+// choices dropped; under a load of seconds 120 and 115 us. The inputs are not __restrict__, so that they are
 // read by plain (coherent) loads: the grid before may still have been writing them.
 constexpr int kCombineThreads = 128;
 
@@ -276,8 +278,9 @@ __global__ void __launch_bounds__(kCombineThreads)
 // contiguous bytes. In a row that starts on an odd element a pair straddles two
 // words: the second comes from the next lane. Nothing behind a row's last column is
 // read (a pair that ends the row is read as single values). Eight pairs a lane and two
-// rows at a time measured best: 5387 x 8 rows of 1307 columns 34 us (four pairs, four
-// rows 44 us; eight neighbouring columns a thread 53 us), 9456 rows of 5065 54 us.
+// rows at a time measured best: 5387 x 8 rows of 1307 columns 35 us (four pairs, four
+// rows 44 us; eight neighbouring columns a thread 53 us), 9456 rows of 5065 54 us. Half
+// of HBM's rate: 4-byte accesses instead of 16-byte ones bound it.
 constexpr int kAnyPairs = 8, kAnyRows = 2;
 __global__ void __launch_bounds__(kCombineThreads, 8)
     expert_combine_any_kernel(const uint16_t* Y, int64_t T, int64_t N, int64_t ldy,

@@ -182,8 +182,9 @@ spense_status search_mx4_plan(int64_t E, int n_tiles, int kblocks, int64_t T, bo
   pl.nacc = pl.split == 1 && 2 * pl.npad + 4 * sf_cols <= 512 ? 2 : 1;
   pl.stages = std::min(pl.stages, (512 - pl.nacc * pl.npad) / sf_cols);
   // Small tiles: two blocks a stage, which halves the waits and signals a block costs
-  // the issuing warp (10240x5120 at one row 8.7 -> 7.5 us, 64-expert decode 37.9 ->
-  // 36.2 us; with more than 64 rows the products cover them: the same either way).
+  // the issuing warp (10240x5120 at one row 8.7 -> 7.5 us in the run that compared
+  // them, 64-expert decode 37.9 -> 36.2 us; with more than 64 rows the products cover
+  // them: the same either way).
   pl.bps = 1;
   if (!pl.pair && pl.npad <= 64 && pl.stages >= 6) {
     pl.bps = 2;

@@ -35,12 +35,15 @@
 // order from a launch in front. Warps 8-11 are a second set of epilogue warps.
 //
 // Bound: up to some 250 rows by the weights' way from HBM (0.53 bytes an element:
-// 64 experts 2560x5120 at 32 rows 36.2 us, 0.88 of the measured copy rate; 128
-// experts 2560x2048 at 509 rows 59.3 us, 0.92), for few weights by the 3.2 us around
-// the blocks and a CTA's 0.25 us a block (10240x5120 at one row 7.5 us), beyond by the
-// tensor pipe and the power cap (51200x5120 at 8192 rows 824 us, 5.2 PFLOP/s; 5120x5120
-// at 4096 rows 47 us, 4.6), for K of a few blocks by the L2 (20480x2560 at 16384 rows
-// 10.4 TB/s of tiles in and 1.7 of Y out).
+// 64 experts 2560x5120 at 32 rows 37 us, 0.86 of the measured copy rate; 128 experts
+// 2560x2048 at 509 rows 61 us, 0.90), for few weights by the 3.2 us around the blocks
+// and a CTA's 0.25 us a block (10240x5120 at one row 8.8 us: 80 CTAs of 20 blocks, since
+// the device holds 74 clusters of two and not 80), beyond by the tensor pipe and the
+// power cap (51200x5120 at 8192 rows 850 us, 5.0 PFLOP/s; 5120x5120 at 4096 rows 44 us,
+// 4.9, and 53 under load), for K of a few blocks by the drain of a pair tile's one
+// accumulator beside its products (32 experts 5120x2560 at 32768 rows 250 us, 3.4
+// PFLOP/s; the tensor pipe is active for 58 % of a launch, 75 % at twice the K) and the
+// L2 (20480x2560 at 16384 rows 10.4 TB/s of tiles in and 1.7 of Y out).
 //
 // Every wait is bounded (1.5 s); on expiry the kernel records a code in the
 // workspace's status word and all roles leave their loops.

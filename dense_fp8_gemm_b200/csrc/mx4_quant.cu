@@ -66,7 +66,8 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* f) {
 //     shared memory, eight rows' words of a column group (32 bytes) at a time:
 //     written one by one they were twice as many requests as the codes. 32768
 //     gathered rows of 5120 take 55 us (the rows' four readings from L2 bound it; with
-//     eight columns a thread and single words 90 us), 8192 rows in order 18 us.
+//     eight columns a thread and single words 90 us), 8192 rows in order 17.4 us (f16
+//     the same, f32 29 us, which is HBM's rate; gathered f16 56 us, f32 94).
 //   else (few rows): the eight warps take eight pieces of one row, so a token's
 //     5120 columns are two CTAs with one round of loads.
 template <bool kWide>
@@ -219,7 +220,8 @@ __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&v)[8]) 
 // Dequantiser. A thread takes 16 columns (half a block: one scale, 32 bytes of bf16
 // output in one store when the output is 32-byte aligned), a warp 512 columns of a
 // row; kWide: eight rows a CTA, two pieces a warp, all loads first; else eight
-// pieces of one row. 32768 rows of 5120 take 71 us, 6.0 TB/s (16-byte stores 86 us).
+// pieces of one row. 32768 rows of 5120 take 71 us, 6.0 TB/s (16-byte stores 86 us);
+// as fp32, whose 64 bytes a thread leave in 16-byte stores, 178 us, 4.3 TB/s.
 //
 // Every value is exact in the output type (two significant bits; 2^-128 at least)
 // below 2^128; larger ones (4 and 6 times 2^126, 2 and more times 2^127), which the
