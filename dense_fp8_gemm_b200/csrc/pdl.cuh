@@ -28,17 +28,9 @@ __device__ __forceinline__ uint32_t ld_dep(const uint32_t* p) {
 __device__ __forceinline__ int32_t ld_dep(const int32_t* p) {
   return static_cast<int32_t>(ld_dep(reinterpret_cast<const uint32_t*>(p)));
 }
-__device__ __forceinline__ float ld_dep(const float* p) {
-  return __uint_as_float(ld_dep(reinterpret_cast<const uint32_t*>(p)));
-}
 __device__ __forceinline__ long long ld_dep(const long long* p) {
   long long v;
   asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint16_t ld_dep(const uint16_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint8_t ld_dep(const uint8_t* p) {
